@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "wq_internal.h"
@@ -143,6 +144,65 @@ int pack_common(int fmt, const float* W, int64_t N, int64_t K, void* packed, voi
   if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return WQ_ERR_ALIGN;
   return fn(W, N, K, reinterpret_cast<uint8_t*>(packed), reinterpret_cast<uint8_t*>(scales),
             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int check_cache(const wq_kv_cache* c, KvArgs& a) {
+  if (!c) return WQ_ERR_ARG;
+  if (c->fmt != WQ_Q4_0 && c->fmt != WQ_NVFP4) return WQ_ERR_FMT;
+  if (c->heads < 1 || c->pages < 0 || c->page_size < 0 || (c->table && c->table_ld < 0)) return WQ_ERR_ARG;
+  if ((c->dim != 64 && c->dim != 128) || c->heads > 65535) return WQ_ERR_SHAPE;
+  if (c->page_size == 0 || c->page_size % 16 != 0 || c->page_size > (1 << 30) || c->pages > (int64_t(1) << 31))
+    return WQ_ERR_SHAPE;
+  if (c->table && c->table_ld > (int64_t(1) << 30)) return WQ_ERR_SHAPE;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return WQ_ERR_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+    return WQ_ERR_ALIGN;
+  if (((uintptr_t)c->table & 3u) || ((uintptr_t)c->k_g & 3u) || ((uintptr_t)c->v_g & 3u)) return WQ_ERR_ALIGN;
+  a.codes[0] = reinterpret_cast<uint8_t*>(c->k_codes);
+  a.codes[1] = reinterpret_cast<uint8_t*>(c->v_codes);
+  a.scales[0] = reinterpret_cast<uint8_t*>(c->k_scales);
+  a.scales[1] = reinterpret_cast<uint8_t*>(c->v_scales);
+  a.g[0] = c->fmt == WQ_NVFP4 ? c->k_g : nullptr;
+  a.g[1] = c->fmt == WQ_NVFP4 ? c->v_g : nullptr;
+  a.table = c->table;
+  a.table_ld = c->table_ld;
+  a.pages = c->pages;
+  a.page_size = (int32_t)c->page_size;
+  a.fmt = c->fmt;
+  a.heads = c->heads;
+  a.dim = c->dim;
+  a.capacity = c->table ? c->table_ld * c->page_size : c->page_size;
+  if (a.capacity > 0x7FFFFFF0) a.capacity = 0x7FFFFFF0;  // positions are int32
+  return WQ_OK;
+}
+
+int check_heads(const wq_heads* h, size_t esz, HeadsArg& a) {
+  if (!h || !h->p || h->batch < 0 || h->token < 0 || h->head < 0) return WQ_ERR_ARG;
+  if (!aligned16(h->p) || ((uint64_t)h->batch * esz) % 16 || ((uint64_t)h->token * esz) % 16 ||
+      ((uint64_t)h->head * esz) % 16)
+    return WQ_ERR_ALIGN;
+  a = HeadsArg{h->p, h->batch, h->token, h->head};
+  return WQ_OK;
+}
+
+bool too_many(int64_t batch, int64_t tokens) {
+  return batch > 0x7FFFFFFF || tokens > 0x7FFFFFFF || batch * tokens > 0x7FFFFFFF;
+}
+
+// The part of an append or read call that the two share; *rows: whether there is anything to do.
+int check_move(const wq_kv_cache* cache, int64_t batch, int64_t tokens, const int32_t* start, const int32_t* counts,
+               KvMoveArgs& a, bool* rows) {
+  int rc = check_cache(cache, a.kv);
+  if (rc != WQ_OK) return rc;
+  if (batch < 0 || tokens < 0) return WQ_ERR_ARG;
+  if (too_many(batch, tokens) || (!cache->table && batch > cache->pages)) return WQ_ERR_SHAPE;
+  if (((uintptr_t)start & 3u) || ((uintptr_t)counts & 3u)) return WQ_ERR_ALIGN;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.start = start;
+  a.counts = counts;
+  *rows = batch > 0 && tokens > 0;
+  return WQ_OK;
 }
 
 }  // namespace
@@ -324,6 +384,72 @@ int wq_linear(const void* x, const void* packed, const void* scales, int fmt, in
   return wq_linear_ex(x, packed, scales, fmt, M, N, K, bias, y, 0u, stream);
 }
 
+int wq_kv_append(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t batch, int64_t tokens,
+                 const int32_t* start, const int32_t* counts, void* stream) {
+  KvMoveArgs a{};
+  bool rows = false;
+  int rc = check_move(cache, batch, tokens, start, counts, a, &rows);
+  if (rc != WQ_OK || !rows) return rc;
+  if ((rc = check_heads(k, 2, a.x[0])) != WQ_OK || (rc = check_heads(v, 2, a.x[1])) != WQ_OK) return rc;
+  return kv_append(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t batch, int64_t tokens,
+               const int32_t* start, const int32_t* counts, unsigned flags, void* stream) {
+  if (flags & ~(unsigned)WQ_FLAG_OUT_F32) return WQ_ERR_ARG;
+  KvMoveArgs a{};
+  bool rows = false;
+  int rc = check_move(cache, batch, tokens, start, counts, a, &rows);
+  if (rc != WQ_OK || !rows) return rc;
+  a.f32 = (flags & WQ_FLAG_OUT_F32) != 0;
+  if (!k && !v) return WQ_ERR_ARG;
+  if (k && (rc = check_heads(k, a.f32 ? 4 : 2, a.x[0])) != WQ_OK) return rc;
+  if (v && (rc = check_heads(v, a.f32 ? 4 : 2, a.x[1])) != WQ_OK) return rc;
+  return kv_read(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
+                                 int64_t max_len) {
+  KvArgs kv{};
+  if (check_cache(cache, kv) != WQ_OK || batch <= 0 || tokens <= 0 || too_many(batch, tokens) || max_len < 0 ||
+      q_heads <= 0 || q_heads > 65535 || q_heads % kv.heads != 0)
+    return 0;
+  return attend_workspace(kv, batch, tokens, q_heads, max_len);
+}
+
+int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
+              int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
+              float scale, int64_t window, unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (flags & ~(unsigned)(WQ_FLAG_OUT_F32 | WQ_FLAG_CAUSAL)) return WQ_ERR_ARG;
+  AttendArgs a{};
+  int rc = check_cache(cache, a.kv);
+  if (rc != WQ_OK) return rc;
+  a.causal = (flags & WQ_FLAG_CAUSAL) != 0;
+  a.f32 = (flags & WQ_FLAG_OUT_F32) != 0;
+  if (batch < 0 || tokens < 0 || q_heads < 0 || max_len < 0 || window < 0 || (window > 0 && !a.causal)) return WQ_ERR_ARG;
+  if (!(scale > -INFINITY && scale < INFINITY)) return WQ_ERR_ARG;
+  if (too_many(batch, tokens) || (!cache->table && batch > cache->pages) || q_heads > 65535 || q_heads % a.kv.heads != 0) return WQ_ERR_SHAPE;
+  if (batch == 0 || tokens == 0 || q_heads == 0) return WQ_OK;
+  if (!lens) return WQ_ERR_ARG;
+  if (((uintptr_t)lens & 3u) || ((uintptr_t)counts & 3u) || ((uintptr_t)lse & 3u)) return WQ_ERR_ALIGN;
+  if ((rc = check_heads(q, 2, a.q)) != WQ_OK || (rc = check_heads(out, a.f32 ? 4 : 2, a.out)) != WQ_OK) return rc;
+  const size_t need = attend_workspace(a.kv, batch, tokens, q_heads, max_len);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return WQ_ERR_ARG;
+  if (need > 0 && !aligned16(workspace)) return WQ_ERR_ALIGN;
+  a.lse = lse;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.lens = lens;
+  a.counts = counts;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.window = window;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return attend(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int wq_selftest_timeout(uint32_t polls, void* stream) {
   if (polls < 1 || polls > (1u << 20)) return WQ_ERR_ARG;
   return wq::selftest_timeout(polls, reinterpret_cast<cudaStream_t>(stream));
@@ -340,8 +466,8 @@ int wq_selftest_encoders(const float* in, int64_t n, uint8_t* out, void* stream)
 int wq_last_device_status(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
   int worst = WQ_OK;
-  const int parts[6] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
-                        take_status_w4a4(), take_status_w4a16()};
+  const int parts[8] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
+                        take_status_w4a4(), take_status_w4a16(), take_status_kv(), take_status_attend()};
   for (int v : parts)
     if (v != WQ_OK) worst = v;
   return worst;

@@ -107,6 +107,51 @@ int take_status_w4a4();
 int linear_w4a16_tc(const LinearArgs& a, cudaStream_t s, int* rc);
 int take_status_w4a16();
 
+// ---- 4-bit KV cache (wq_kv.cu) and attention over it (wq_attend.cu)
+struct KvArgs {
+  uint8_t* codes[2];    // K, V
+  uint8_t* scales[2];
+  const float* g[2];    // NVFP4 global scales, NULL = 1
+  const int32_t* table; // NULL: sequence b owns page b
+  int64_t table_ld;
+  int64_t pages;
+  int64_t capacity;     // tokens per sequence
+  int32_t page_size, fmt, heads, dim;
+};
+struct HeadsArg {
+  void* p;
+  int64_t batch, token, head;  // element strides
+};
+struct KvMoveArgs {
+  KvArgs kv;
+  HeadsArg x[2];        // K, V rows (x[i].p == NULL: not wanted)
+  int64_t batch, tokens;
+  const int32_t* start;
+  const int32_t* counts;
+  bool f32;
+};
+int kv_append(const KvMoveArgs& a, cudaStream_t s);
+int kv_read(const KvMoveArgs& a, cudaStream_t s);
+int take_status_kv();
+
+struct AttendArgs {
+  KvArgs kv;
+  HeadsArg q, out;
+  float* lse;
+  int64_t batch, tokens, q_heads;
+  const int32_t* lens;
+  const int32_t* counts;
+  int64_t max_len;
+  float scale;
+  int64_t window;       // 0: none
+  bool causal, f32;
+  void* workspace;
+  size_t workspace_bytes;
+};
+size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len);
+int attend(const AttendArgs& a, cudaStream_t s);
+int take_status_attend();
+
 // driver entry point for tensor-map encoding (resolved once through the runtime)
 bool encode_tmap_2d(void* tmap, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);

@@ -25,7 +25,7 @@ WQ_NF4, WQ_NVFP4, WQ_NVFP4_W4A4, WQ_Q4_0, WQ_Q8_0, WQ_Q4_1, WQ_Q5_0, WQ_FP8 = 1,
 FMT = {"nf4": WQ_NF4, "nvfp4": WQ_NVFP4, "nvfp4_w4a4": WQ_NVFP4_W4A4, "q4_0": WQ_Q4_0, "q8_0": WQ_Q8_0,
        "q4_1": WQ_Q4_1, "q5_0": WQ_Q5_0, "fp8": WQ_FP8}
 WQ_OK, WQ_ERR_ARG, WQ_ERR_SHAPE, WQ_ERR_ALIGN, WQ_ERR_FMT, WQ_ERR_CUDA, WQ_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
-WQ_FLAG_OUT_F32, WQ_FLAG_WEIGHTS_STATIC, WQ_FLAG_FORCE_SIMT = 1, 2, 4
+WQ_FLAG_OUT_F32, WQ_FLAG_WEIGHTS_STATIC, WQ_FLAG_FORCE_SIMT, WQ_FLAG_CAUSAL = 1, 2, 4, 8
 
 
 class wq_act_nvfp4(ctypes.Structure):
@@ -51,6 +51,20 @@ class wq_problem_ex(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("nout", ctypes.c_int), ("out", wq_out * WQ_OUT_MAX)]
 
+
+class wq_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_g", ctypes.c_void_p), ("v_g", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("fmt", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
+class wq_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
 _P, _I64, _I, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint
 _SIGS = {
     "wq_packed_bytes": (ctypes.c_size_t, [_I, _I64, _I64]),
@@ -68,6 +82,11 @@ _SIGS = {
     "wq_linear_ex": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _U, _P]),
     "wq_linear_grouped": (_I, [_P, _I, _I, _U, _P]),
     "wq_linear_grouped_ex": (_I, [_P, _I, _I, _U, _P]),
+    "wq_kv_append": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P]),
+    "wq_kv_read": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _U, _P]),
+    "wq_attend_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64, _I64, _I64]),
+    "wq_attend": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I64, _U, _P,
+                       ctypes.c_size_t, _P]),
     "wq_last_device_status": (_I, []),
     "wq_status_string": (ctypes.c_char_p, [_I]),
     "wq_kernel_launches": (ctypes.c_uint64, []),
@@ -218,6 +237,125 @@ def linear_grouped_ex(problems, fmt, out_f32=False, weights_static=False, stream
     flags = (WQ_FLAG_OUT_F32 if out_f32 else 0) | (WQ_FLAG_WEIGHTS_STATIC if weights_static else 0)
     _check("wq_linear_grouped_ex", lib.wq_linear_grouped_ex(ctypes.cast(arr, ctypes.c_void_p), len(problems),
                                                             _fmt(fmt), flags, _stream(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit KV cache
+class KVCache:
+    """A 4-bit K/V cache in the caller's CUDA tensors (layouts in include/wq.h).
+
+    k_codes, v_codes: uint8 [pages, heads, page_size, dim / 2]; k_scales, v_scales: float16
+    [pages, heads, page_size, dim / 32] (fmt 'q4_0') or uint8 E4M3 bytes [pages, heads, page_size,
+    dim / 16] ('nvfp4'); table: int32 [batch, n] page numbers, or None (sequence b owns page b);
+    k_g, v_g: fp32 [1] static global scales of 'nvfp4', or None for 1."""
+
+    def __init__(self, fmt, k_codes, k_scales, v_codes, v_scales, table=None, k_g=None, v_g=None):
+        f = _fmt(fmt)
+        if f not in (WQ_Q4_0, WQ_NVFP4):
+            raise WQError("KVCache", WQ_ERR_FMT)
+        pages, heads, page_size, half = k_codes.shape
+        dim, stype = 2 * half, torch.float16 if f == WQ_Q4_0 else torch.uint8
+        sshape = (pages, heads, page_size, dim // (32 if f == WQ_Q4_0 else 16))
+        for t in (k_codes, v_codes):
+            assert t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous() and t.shape == k_codes.shape
+        for t in (k_scales, v_scales):
+            assert t.is_cuda and t.dtype == stype and t.is_contiguous() and tuple(t.shape) == sshape
+        for t in (k_g, v_g):
+            assert t is None or (t.is_cuda and t.dtype == torch.float32 and t.numel() == 1)
+        assert table is None or (table.is_cuda and table.dtype == torch.int32 and table.dim() == 2
+                                 and table.is_contiguous())
+        self.fmt, self.pages, self.heads, self.page_size, self.dim = f, pages, heads, page_size, dim
+        self.capacity = page_size if table is None else table.shape[1] * page_size
+        self.batch = pages if table is None else table.shape[0]
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, table, k_g, v_g)
+        self.device = k_codes.device
+        opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = wq_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                             opt(k_g), opt(v_g), opt(table), 0 if table is None else table.shape[1], pages, page_size,
+                             f, heads, dim)
+        self.ref = ctypes.cast(ctypes.pointer(self.c), ctypes.c_void_p)
+
+
+def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, device="cuda"):
+    """A KVCache in new tensors whose every row reads as zero."""
+    f = _fmt(fmt)
+    zero = 0x88 if f == WQ_Q4_0 else 0
+    codes = [torch.full((pages, heads, page_size, dim // 2), zero, dtype=torch.uint8, device=device) for _ in range(2)]
+    sdim, stype = (dim // 32, torch.float16) if f == WQ_Q4_0 else (dim // 16, torch.uint8)
+    scales = [torch.zeros((pages, heads, page_size, sdim), dtype=stype, device=device) for _ in range(2)]
+    return KVCache(fmt, codes[0], scales[0], codes[1], scales[1], table, k_g, v_g)
+
+
+def _heads(t, dtype):
+    """[batch, token, head, dim] view -> wq_heads (dim contiguous; other strides as they are)."""
+    assert t.is_cuda and t.dtype == dtype and t.stride(3) == 1
+    s = t.stride()
+    return wq_heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _index(t, batch):
+    assert t is None or (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and t.numel() == batch)
+    return None if t is None else t.data_ptr()
+
+
+def kv_append(cache, k, v, start=None, counts=None, stream=None):
+    """Quantise k, v (bf16 [batch, tokens, heads, dim] views) into positions start[b] .. start[b] + counts[b] - 1
+    of the cache (int32 CUDA tensors; None: 0, and all tokens)."""
+    batch, tokens, heads, dim = k.shape
+    assert v.shape == k.shape and heads == cache.heads and dim == cache.dim and batch <= cache.batch
+    _check("wq_kv_append", lib.wq_kv_append(cache.ref, ctypes.byref(_heads(k, torch.bfloat16)),
+                                            ctypes.byref(_heads(v, torch.bfloat16)), batch, tokens,
+                                            _index(start, batch), _index(counts, batch), _stream(stream)))
+
+
+def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, stream=None):
+    """The values at start[b] + i, i < counts[b], of each sequence -> k, v [batch, tokens, heads, dim] (bf16, or
+    fp32 with out_f32); rows from counts[b] on are zero.  batch defaults to start's or counts' length, else the
+    cache's number of sequences."""
+    if batch is None:
+        batch = cache.batch if start is None and counts is None else (counts if start is None else start).numel()
+    assert batch <= cache.batch
+    dt = torch.float32 if out_f32 else torch.bfloat16
+    k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
+    v = torch.empty_like(k)
+    _check("wq_kv_read", lib.wq_kv_read(cache.ref, ctypes.byref(_heads(k, dt)), ctypes.byref(_heads(v, dt)), batch, tokens,
+                                        _index(start, batch), _index(counts, batch), WQ_FLAG_OUT_F32 if out_f32 else 0,
+                                        _stream(stream)))
+    return k, v
+
+
+def attend_workspace_bytes(cache, batch, tokens, q_heads, max_len=0):
+    return int(lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len))
+
+
+def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_len=0, out=None, out_f32=False,
+           return_lse=False, workspace=None, stream=None):
+    """Attention of q (bf16 [batch, tokens, q_heads, dim] view) over the lens[b] cached tokens of each sequence.
+
+    lens, counts: int32 CUDA tensors [batch]; the last counts[b] (None: all of `tokens`) cached positions are
+    q's.  causal: query i sees positions up to its own; window > 0: only the last `window` of those.  scale:
+    default dim^-0.5.  max_len: a host-side upper bound of lens if one is known (plans the split of long
+    sequences).  out: a [batch, tokens, q_heads, dim] view to write to.  Returns out, or (out, lse) with
+    lse fp32 [batch, tokens, q_heads].  Rows that see nothing give 0 and -inf.  workspace: a uint8 tensor of
+    attend_workspace_bytes() bytes; allocated for the call on the current stream when None (pass one with
+    an explicit stream)."""
+    batch, tokens, q_heads, dim = q.shape
+    assert dim == cache.dim and batch <= cache.batch
+    dt = torch.float32 if out_f32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((batch, tokens, q_heads, dim), dtype=dt, device=q.device)
+    assert out.shape == q.shape
+    lse = torch.empty((batch, tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    need = lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check("wq_attend", lib.wq_attend(cache.ref, ctypes.byref(_heads(q, torch.bfloat16)), ctypes.byref(_heads(out, dt)),
+                                      None if lse is None else lse.data_ptr(), batch, tokens, q_heads,
+                                      _index(lens, batch), _index(counts, batch), max_len,
+                                      dim ** -0.5 if scale is None else scale, window,
+                                      (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
+                                      None if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel(), _stream(stream)))
+    return (out, lse) if return_lse else out
 
 
 def last_device_status():

@@ -243,10 +243,109 @@ typedef struct wq_problem_ex {
 
 int wq_linear_grouped_ex(const wq_problem_ex* problems, int count, int fmt, unsigned flags, void* stream);
 
+/* ---------------------------------------------------------------- 4-bit KV cache
+ * A cache of K and V rows in one of the 4-bit formats whose scales are local to
+ * a token, so that tokens can be appended one by one: WQ_Q4_0 (fp16 d per 32
+ * elements, value (c - 8) * d) or WQ_NVFP4 (E4M3 scale per 16 elements and one
+ * static fp32 g for K and one for V, value (E2M1(c) * s) * g).  Blocks run along
+ * the head's `dim` elements.  9/16 byte per element in either format.
+ *
+ * Storage.  `pages` pages of `page_size` tokens:
+ *   codes   [pages, heads, page_size, dim / 2] bytes, element 2j of a row in the
+ *           low nibble of byte j
+ *   scales  WQ_Q4_0:  fp16 d      [pages, heads, page_size, dim / 32]
+ *           WQ_NVFP4: E4M3 bytes  [pages, heads, page_size, dim / 16]
+ * (a page is bit for bit the packed codes and scales of a weight [heads *
+ * page_size, dim] of that format).  Position t of sequence b lies in page
+ * table[b * table_ld + t / page_size] at t % page_size; with table == NULL the
+ * sequence owns page b whole (a contiguous slab per sequence).  The capacity of a
+ * sequence is table_ld * page_size, or page_size without a table.
+ *
+ * Rules: dim is 64 or 128; page_size is a multiple of 16; heads >= 1; codes and
+ * scales 16-byte aligned, k_g / v_g / table 4-byte aligned.  k_g / v_g are used by
+ * WQ_NVFP4 only; NULL stands for 1.  The struct lives in HOST memory; its pointers
+ * are device pointers.
+ *
+ * Positions and lengths come from device memory, so the host cannot check them:
+ * the kernels do.  A position outside a sequence's capacity, or a table entry
+ * outside [0, pages), is neither read nor written (kv_append drops the token,
+ * kv_read gives zeros, attend treats the token as not there), and
+ * wq_last_device_status reports WQ_ERR_ARG.                                       */
+typedef struct wq_kv_cache {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  const float* k_g;        /* WQ_NVFP4: one fp32 each, or NULL for 1            */
+  const float* v_g;
+  const int32_t* table;    /* [batch, table_ld] page numbers, or NULL           */
+  int64_t table_ld;
+  int64_t pages;
+  int64_t page_size;       /* tokens per page                                   */
+  int32_t fmt;             /* WQ_Q4_0 or WQ_NVFP4                               */
+  int32_t heads;           /* K/V heads                                         */
+  int32_t dim;             /* elements per head: 64 or 128                      */
+} wq_kv_cache;
+
+/* A [batch, token, head, dim] array by its strides in elements (dim is
+ * contiguous): a column range of a fused projection's output is one.  p and
+ * every stride times the element size are multiples of 16 bytes; strides are not
+ * negative.  Lives in HOST memory; p is a device pointer.                         */
+typedef struct wq_heads {
+  void* p;
+  int64_t batch, token, head;
+} wq_heads;
+
+/* wq_kv_append: quantise k and v (bf16) into the cache: token i of sequence b,
+ * 0 <= i < counts[b], goes to position start[b] + i.  start NULL: 0; counts NULL:
+ * `tokens` for every sequence (values outside [0, tokens] are clamped).  Codes and
+ * scales equal those of wq_pack_q4_0 / wq_quant_act_nvfp4 (static g) on the same
+ * values.  A NaN in a q4_0 block makes the block read back as NaN; an NVFP4
+ * block cannot hold one.  Tokens of one call must not share a position.
+ *
+ * wq_kv_read: decode positions start[b] + i, 0 <= i < counts[b], to k and v
+ * [batch, tokens, heads, dim] (bf16 rounded to nearest even, or fp32 with
+ * WQ_FLAG_OUT_F32); rows from counts[b] on are zero.  k or v may be NULL.
+ *
+ * batch * tokens < 2^31.                                                         */
+int wq_kv_append(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t batch, int64_t tokens,
+                 const int32_t* start, const int32_t* counts, void* stream);
+int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t batch, int64_t tokens,
+               const int32_t* start, const int32_t* counts, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------- attention over the cache
+ * wq_attend: out = softmax(scale * q . K^T) . V over the cached tokens, per
+ * sequence and query head.  q is bf16 [batch, tokens, q_heads, dim]; q_heads is a
+ * multiple of the cache's heads, and query head h reads cache head
+ * h / (q_heads / heads).  lens[b] is the number of tokens that sequence b holds
+ * (those of this call included: append first).  counts as above: the last
+ * counts[b] positions are this call's query tokens; query i sits at position
+ * p = lens[b] - counts[b] + i.
+ *   visible tokens   0 <= t < lens[b]; with WQ_FLAG_CAUSAL also t <= p, and with
+ *                    window > 0 (WQ_FLAG_CAUSAL only) also t > p - window
+ *   out              bf16, or fp32 with WQ_FLAG_OUT_F32, [batch, tokens, q_heads, dim]
+ *   lse              fp32 [batch, tokens, q_heads] dense, or NULL: the natural log
+ *                    of the sum of exp(scale * q . k) over the visible tokens
+ * A row that sees no token, and a row from counts[b] on, gets out = 0 and
+ * lse = -inf.  Cache contents past lens[b] are never used, whatever they hold.
+ * max_len: what the caller knows on the host of lens (an upper bound, used to
+ * plan the split of long sequences only; 0 stands for the capacity).
+ * scale: finite.  Softmax statistics and sums are fp32.
+ *
+ * workspace: wq_attend_workspace_bytes(...) bytes (16-byte aligned, no
+ * initialisation; may be NULL where that is 0) that no other call in flight uses. */
+enum { WQ_FLAG_CAUSAL = 1u << 3 };
+size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
+                                 int64_t max_len);
+int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
+              int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
+              float scale, int64_t window, unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- status
  * wq_last_device_status: synchronises the current device, returns and clears
- * the device-side status word (WQ_OK, or WQ_ERR_TIMEOUT if a kernel abandoned
- * a bounded wait since the last call).  Not for hot loops.
+ * the device-side status word (WQ_OK; WQ_ERR_TIMEOUT if a kernel abandoned a
+ * bounded wait since the last call; WQ_ERR_ARG if a KV cache kernel met a
+ * position or page outside the cache).  Not for hot loops.
  * wq_status_string: a static description of a status code.
  * wq_kernel_launches: number of kernels this library has launched in this
  * process (host-side counter).                                                 */
