@@ -1,8 +1,24 @@
-// wq_attend.cu -- attention over the 4-bit KV cache.
+// wq_attend.cu -- attention over the 4-bit KV cache, few query rows per cached head (decode).
 //
-// One block per query row and head; its warps take the visible tokens in turn, each lane D / 32
-// elements of a token.  Online softmax: m the running maximum of the scores (in base 2), l the sum
-// of 2^(s - m), o the sum of 2^(s - m) v; warps are joined at the end, in order.
+// With x_t the codes of token t, S = scale * Q K^T and O = softmax(S) V are computed from the codes
+// as they lie in the cache.  A block owns one cached head of one sequence, up to 8 * NT query rows
+// (the query heads of the group times the tokens of the call) and a range of tokens; each of its
+// four warps streams 32-token tiles of that range through a ring of its own in shared memory
+// (cp.async: no wait of one warp on another) and keeps its own running maximum m, sum l and O,
+// joined at the end.  The transposed products put tokens (then head elements) on the 16-row side of
+// mma.m16n8k16, so that one to eight query rows fill its 8-column side:
+//   S^T [16 tokens x 8 rows] = K [16 x D] . Q^T [D x 8],    O^T [D x 8 rows] += V^T [D x 16] . P^T [16 x 8].
+// ldmatrix on the packed bytes deals them out as the two A operands need them: plain, a lane gets
+// eight codes of one token; transposed, four codes of each of two tokens, side by side in a register.
+//
+// q4_0, K: a nibble in place is an fp16 subnormal (c * 2^-24, or c * 2^-20 in bits 4 .. 7), exact in the
+// MMA, so unpacking is one AND per two codes; the 2^-4 between the two is folded into Q, the offset of 8 is
+// the accumulator's initial value, -8 * sum(Q) over the block, and d multiplies the block's partial score in
+// fp32.  V: a nibble under the exponent of 1024 less 1032 is c - 8 (the sum over tokens runs over weights
+// that differ by many orders of magnitude, so an offset taken off afterwards would leave its rounding in
+// elements that are small); d multiplies the weight (p and p d are rounded to fp16, 2^-11 each).  NVFP4:
+// E2M1(c) * E4M3(s) is exact in fp16 (6 significant bits), g enters with the softmax scale and the output.
+// Q is scaled per row by a power of two, so that its bf16 values are exact in fp16.
 #include <cuda_runtime.h>
 
 #include "wq_kv.cuh"
@@ -11,91 +27,708 @@ namespace wq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kTile = 32;    // tokens per tile
+constexpr int kStages = 3;   // tiles in a warp's ring
+constexpr int kSms = 152;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kWarps) attend_kernel(AttendArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x / (uint32_t)a.tokens;
-  const int i = (int)(blockIdx.x - (uint32_t)b * (uint32_t)a.tokens);
-  const int hq = blockIdx.y, h = hq / (int)(a.q_heads / a.kv.heads);
+// Bytes of one tile of D-element rows: K and V codes, then K and V scales.
+constexpr int stage_bytes(int D) { return 2 * kTile * (D / 2) + 2 * kTile * kv::scale_bytes(D); }
+constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
+constexpr int q_bytes(int D, int NT) { return NT > 2 ? NT * (D / 32) * 32 * 16 : 0; }
+// Joining the warps: O [warp][row][D], then m and l [warp][row].
+constexpr int join_bytes(int D, int NT) { return kWarps * 8 * NT * (D * 4 + 8); }
+constexpr int smem_bytes(int D, int NT) {
+  return (ring_bytes(D) > join_bytes(D, NT) ? ring_bytes(D) : join_bytes(D, NT)) + q_bytes(D, NT);
+}
+
+struct Params {
+  AttendArgs a;
+  int group;        // query heads per cached head
+  int row_tiles;    // blocks of 8 * NT query rows per cached head
+  int splits;       // blocks that share the tokens of one row tile
+  float* part_o;    // [row tile][split][8 * NT][D] unnormalised outputs
+  float* part_ml;   // [row tile][split][8 * NT][2] their m (base 2) and l
+};
+
+// Byte offset of 16-byte chunk `col` (a block of 32 codes) of token `row` in a tile: the chunks of
+// eight neighbouring rows fall into different banks for ldmatrix.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int row, int col) {
+  return (uint32_t)(row * (D / 2) + ((col ^ ((D == 128 ? row >> 1 : row >> 2) & (D / 32 - 1))) << 4));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// c - 8 of the codes in bits 0 .. 3 and 4 .. 7 of each half, as fp16 pairs: 1024 + c - 1032, and
+// (1024 + 16 c) / 16 - 72, both exact.
+__device__ __forceinline__ void signed_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  lo = add2((w & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+  hi = fma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Four bytes of two E2M1 codes -> four fp16 pairs (low nibble in the low half).
+__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+// Four E4M3 bytes -> two fp16 pairs.
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "mov.b32 {h0, h1}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, h0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h1;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Which of a lane's eight elements of a block pair p of a K operand holds (see the K unpacking).
+template <int FMT>
+__device__ __forceinline__ constexpr int pair_lo(int p) { return FMT == WQ_Q4_0 ? p : 2 * p; }
+template <int FMT>
+__device__ __forceinline__ constexpr int pair_hi(int p) { return FMT == WQ_Q4_0 ? p + 4 : 2 * p + 1; }
+
+// Write one output element.
+__device__ __forceinline__ void put(const AttendArgs& a, int64_t at, float v) {
+  if (a.f32) reinterpret_cast<float*>(a.out.p)[at] = v;
+  else reinterpret_cast<__nv_bfloat16*>(a.out.p)[at] = __float2bfloat16_rn(v);
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(const __grid_constant__ Params p) {
+  constexpr int NB = D / 32;            // 32-element blocks of a row
+  constexpr int kCodes = kTile * (D / 2), kScales = kTile * kv::scale_bytes(D);
+  constexpr bool kQSmem = NT > 2;       // Q fragments live in shared memory instead of registers
+  extern __shared__ __align__(128) uint8_t smem[];
+  const AttendArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+
+  uint32_t x = blockIdx.x;
+  const int split = x % p.splits;
+  x /= p.splits;
+  const int64_t tile_id = x;            // (sequence, cached head, row tile)
+  const int rt = x % p.row_tiles;
+  x /= p.row_tiles;
+  const int h = x % a.kv.heads;
+  const int64_t b = x / a.kv.heads;
+
+  // The rows' tokens and what they see.
   const int n = kv::count_of(a.counts, b, a.tokens);
   int len = max(a.lens[b], 0);
   if (len > a.kv.capacity) {
     if (threadIdx.x == 0) set_status(WQ_STATUS_ARG);
     len = (int)a.kv.capacity;
   }
-  int lo = 0, hi = len;
-  const int64_t p = (int64_t)len - n + i;
-  if (a.causal) hi = (int)min((int64_t)hi, p + 1);
-  if (a.window) lo = (int)max((int64_t)0, p - a.window + 1);
-  if (i >= n) hi = 0;
-  float q[E], o[E];
-  const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token + hq * a.q.head;
+  const int64_t r0 = (int64_t)rt * 8 * NT;                    // first row: token r / group, head r % group
+  const int64_t rows = (int64_t)n * p.group;                  // rows of this sequence
+  auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)len, (int64_t)len - n + i + 1)) : len; };
+  auto lo_of = [&](int64_t i) { return a.window ? (int)max((int64_t)0, (int64_t)len - n + i - a.window + 1) : 0; };
+  const int64_t i_first = r0 / p.group, i_last = min(rows - 1, r0 + 8 * NT - 1) / p.group;
+  const bool any = r0 < rows;
+  const int lo_min = any ? lo_of(i_first) : 0, hi_max = any ? hi_of(i_last) : 0;
+  const int lo_max = any ? lo_of(i_last) : 0, hi_min = any ? hi_of(i_first) : 0;
+  const int tile0 = lo_min / kTile;
+  const int ntiles = hi_max > lo_min ? (hi_max + kTile - 1) / kTile - tile0 : 0;
+  const int per = (ntiles + p.splits - 1) / p.splits;
+  const int t_end = tile0 + min(ntiles, (split + 1) * per);
+  const int t_begin = tile0 + min(ntiles, split * per) + warp;
+
+  const uint32_t ring = smem_u32(smem) + warp * kStages * stage_bytes(D);
+  uint8_t* qs = smem + (ring_bytes(D) > join_bytes(D, NT) ? ring_bytes(D) : join_bytes(D, NT));
+
+  // ---------------------------------------------------------------- streaming tiles
+  // Row number of the tile's half (lane & 1), -1: past the end, -2: no such page.
+  auto locate = [&](int tile) -> int64_t {
+    const int t = tile * kTile + 16 * (lane & 1);
+    if (tile >= t_end || t >= hi_max) return -1;
+    int64_t page = b;
+    int off = t;
+    if (a.kv.table) {
+      const int pg = (unsigned)t / (unsigned)a.kv.page_size;
+      off = t - pg * a.kv.page_size;
+      page = a.kv.table[b * a.kv.table_ld + pg];
+    }
+    if (page < 0 || page >= a.kv.pages) {
+      set_status(WQ_STATUS_ARG);
+      return -2;
+    }
+    return (page * a.kv.heads + h) * (int64_t)a.kv.page_size + off;
+  };
+  uint32_t missing = 0;                 // per stage and half: the page is not there
+  auto issue = [&](int tile, int stage, int64_t mine) {
+    const int64_t row[2] = {__shfl_sync(0xFFFFFFFFu, mine, 0), __shfl_sync(0xFFFFFFFFu, mine, 1)};
+    missing = (missing & ~(3u << (2 * stage))) | ((row[0] == -2 ? 1u : 0u) | (row[1] == -2 ? 2u : 0u)) << (2 * stage);
+    const uint32_t dst = ring + stage * stage_bytes(D);
+    constexpr int kPer = kTile * NB / 32;            // 16-byte chunks per lane
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    q[j] = bf16_bits_to_f32(qp[lane * E + j]);
-    o[j] = 0.0f;
+    for (int j = 0; j < kPer; ++j) {
+      const int c = j * 32 + lane, r = c / NB, col = c % NB, half = r >> 4;
+      const bool in = row[half] >= 0 && tile * kTile + r < hi_max;
+      const int64_t at = in ? (row[half] + (r & 15)) * (D / 2) + col * 16 : 0;
+      cp16(dst + tile_at<D>(r, col), a.kv.codes[0] + at, in ? 16 : 0);
+      cp16(dst + kCodes + tile_at<D>(r, col), a.kv.codes[1] + at, in ? 16 : 0);
+    }
+    const int half = lane >> 4;
+    const bool in = (half ? row[1] : row[0]) >= 0 && tile * kTile + lane < hi_max;
+    const int64_t at = in ? ((half ? row[1] : row[0]) + (lane & 15)) * kv::scale_bytes(D) : 0;
+    cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + lane * kv::scale_bytes(D), a.kv.scales[0] + at,
+                                 in ? kv::scale_bytes(D) : 0);
+    cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + kScales + lane * kv::scale_bytes(D), a.kv.scales[1] + at,
+                                 in ? kv::scale_bytes(D) : 0);
+  };
+  int64_t next = locate(t_begin);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (t_begin + s * kWarps < t_end) issue(t_begin + s * kWarps, s, next);
+    cp_commit();
+    next = locate(t_begin + (s + 1) * kWarps);
   }
-  const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f, vg = FMT == WQ_NVFP4 && a.kv.g[1] ? *a.kv.g[1] : 1.0f;
-  const float c = a.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.0f;
-  for (int t = lo + warp; t < hi; t += kWarps) {
-    const int64_t row = kv::row_of(a.kv, b, t, h);
-    if (row < 0) continue;
-    float k[8], v[8];
-    const int e = lane * E, sh = 4 * (e & 7);
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(a.kv.codes[0] + row * (D / 2) + (e & ~7) / 2);
-    const uint32_t vw = *reinterpret_cast<const uint32_t*>(a.kv.codes[1] + row * (D / 2) + (e & ~7) / 2);
-    kv::decode8<FMT>(kw >> sh, kv::scale_at<FMT>(a.kv.scales[0] + row * kv::scale_bytes(D), e), kg, k);
-    kv::decode8<FMT>(vw >> sh, kv::scale_at<FMT>(a.kv.scales[1] + row * kv::scale_bytes(D), e), vg, v);
-    float s = 0.0f;
+
+  // ---------------------------------------------------------------- Q
+  // Lane (g, q) holds row 8 j + g's elements 32 blk + 8 q .. + 7.  The row is multiplied by 2^e, which
+  // brings its largest element to 2^12 .. 2^13.
+  uint32_t qf[kQSmem ? 1 : NT][NB][4];
+  float init[NT][FMT == WQ_Q4_0 ? NB : 1][2];   // q4_0: -8 sum(Q) of a block, columns 2q and 2q + 1
+  float fac[NT][2];                             // accumulated score -> score in base 2
+  const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) s = fmaf(q[j], k[j], s);
+  for (int j = 0; j < NT; ++j) {
+    const int64_t r = r0 + 8 * j + g;
+    uint32_t u[NB][4];
+    const bool in = r < rows;
+    const int64_t i = in ? r / p.group : 0;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token +
+                          ((int64_t)h * p.group + (in ? r - i * p.group : 0)) * a.q.head + 8 * q;
+    float amax = 0.0f;
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    s *= c;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = fmaf(l, f, w);
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint4 w = in ? *reinterpret_cast<const uint4*>(src + 32 * blk) : make_uint4(0, 0, 0, 0);
+      u[blk][0] = w.x; u[blk][1] = w.y; u[blk][2] = w.z; u[blk][3] = w.w;
 #pragma unroll
-    for (int j = 0; j < E; ++j) o[j] = fmaf(o[j], f, w * v[j]);
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(bf16_bits_to_f32((u[blk][e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    int e2 = 12 + 127 - (int)(__float_as_uint(amax) >> 23);
+    e2 = amax == 0.0f || amax == INFINITY ? 0 : min(e2, 112);
+    const float up = __uint_as_float((uint32_t)(127 + e2) << 23), down = __uint_as_float((uint32_t)(127 - e2) << 23);
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      float v[8], sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = bf16_bits_to_f32((u[blk][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * up;
+        sum += v[e];
+      }
+      uint32_t f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float k = FMT == WQ_Q4_0 && (e & 1) ? 0.0625f : 1.0f;
+        f[e] = pack_f16x2(v[pair_lo<FMT>(e)] * k, v[pair_hi<FMT>(e)] * k);
+      }
+      if (kQSmem) {
+        if (warp == 0) reinterpret_cast<uint4*>(qs)[(j * NB + blk) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qf[kQSmem ? 0 : j][blk][e] = f[e];
+      }
+      if (FMT == WQ_Q4_0) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        sum *= -8.0f * 5.9604644775390625e-8f;   // -8 * 2^-24
+        init[j][FMT == WQ_Q4_0 ? blk : 0][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * q);
+        init[j][FMT == WQ_Q4_0 ? blk : 0][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * q + 4);
+      }
+    }
+    const float f = a.scale * kLog2e * (FMT == WQ_Q4_0 ? 16777216.0f : kg) * down;
+    fac[j][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * q);
+    fac[j][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * q + 4);
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+  if (kQSmem) __syncthreads();
+
+  // Columns' visible ranges (8 j + 2q and + 1); columns that are no rows count as seeing all.
+  int c_lo[NT][2], c_hi[NT][2];
 #pragma unroll
-  for (int j = 0; j < E; ++j) so[warp][lane * E + j] = o[j];
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t r = r0 + 8 * j + 2 * q + c, i = r / p.group;
+      c_lo[j][c] = r < rows ? lo_of(i) : 0;
+      c_hi[j][c] = r < rows ? hi_of(i) : hi_max;
+    }
+
+  float o[NT][2 * NB][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    m[j][0] = m[j][1] = -INFINITY;
+    l[j][0] = l[j][1] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int d = 0; d < 2 * NB; ++d) o[j][d][k] = 0.0f;
+  }
+
+  // ---------------------------------------------------------------- tiles
+  int stage = 0;
+  for (int tile = t_begin; tile < t_end; tile += kWarps) {
+    {
+      const int ahead = tile + (kStages - 1) * kWarps;
+      int s = stage + kStages - 1;
+      if (s >= kStages) s -= kStages;
+      if (ahead < t_end) issue(ahead, s, next);
+      cp_commit();
+      next = locate(ahead + kWarps);
+    }
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t base = ring + stage * stage_bytes(D);
+    const uint8_t* gen = smem + (base - smem_u32(smem));
+
+    // ---- scores of 2 x 16 tokens
+    float s[2][NT][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[u][j][k] = 0.0f;
+    uint32_t kw[2][2][4];               // [group][token g or g + 8][block]
+    float kd[2][2][FMT == WQ_Q4_0 ? NB : 1];
+    uint32_t ks[2][2][FMT == WQ_NVFP4 ? NB : 1];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (NB == 4) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) ldsm(kw[u][hf], base + tile_at<D>(16 * u + 8 * hf + (lane & 7), lane >> 3));
+      } else {
+        uint32_t r[4];
+        ldsm(r, base + tile_at<D>(16 * u + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+        kw[u][0][0] = r[0]; kw[u][0][1] = r[1]; kw[u][1][0] = r[2]; kw[u][1][1] = r[3];
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* sp = gen + 2 * kCodes + (16 * u + 8 * hf + g) * kv::scale_bytes(D);
+        uint32_t w[2];
+        if (NB == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(sp);
+          w[0] = v.x; w[1] = v.y;
+        } else {
+          w[0] = w[1] = *reinterpret_cast<const uint32_t*>(sp);
+        }
+        if (FMT == WQ_Q4_0) {
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
+            kd[u][hf][FMT == WQ_Q4_0 ? blk : 0] = f16_bits_to_f32((w[blk >> 1] >> (16 * (blk & 1))) & 0xFFFFu);
+        } else {
+          // the word of lane q lies in the 16-block q >> 1 of its 32 elements
+          const uint32_t sel = (q >> 1) ? 0x3311u : 0x2200u;
+#pragma unroll
+          for (int pr = 0; pr < NB / 2; ++pr)
+            e4m3_pairs(__byte_perm(w[pr], 0, sel), ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr : 0], ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr + 1 : 0]);
+        }
+      }
+    }
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      uint32_t av[2][2][4];             // [group][token g or g + 8][pair]
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t w = kw[u][hf][blk];
+          if (FMT == WQ_Q4_0) {
+            av[u][hf][0] = w & 0x000F000Fu;
+            av[u][hf][1] = w & 0x00F000F0u;
+            av[u][hf][2] = (w >> 8) & 0x000F000Fu;
+            av[u][hf][3] = (w >> 8) & 0x00F000F0u;
+          } else {
+            e2m1_pairs(w, av[u][hf]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) av[u][hf][e] = mul2(av[u][hf][e], ks[u][hf][FMT == WQ_NVFP4 ? blk : 0]);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint32_t f[4];
+        if (kQSmem) {
+          const uint4 v = reinterpret_cast<const uint4*>(qs)[(j * NB + blk) * 32 + lane];
+          f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = qf[kQSmem ? 0 : j][blk][e];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (FMT == WQ_Q4_0) {
+            const int ib = FMT == WQ_Q4_0 ? blk : 0;
+            float c[4] = {init[j][ib][0], init[j][ib][1], init[j][ib][0], init[j][ib][1]};
+            mma(c, av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1]);
+            mma(c, av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[u][j][k] = fmaf(kd[u][k >> 1][ib], c[k], s[u][j][k]);
+          } else {
+            mma(s[u][j], av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1]);
+            mma(s[u][j], av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+          }
+        }
+      }
+    }
+
+    // ---- online softmax: c[0], c[1] are token g's columns 2q, 2q + 1, c[2], c[3] token g + 8's
+    const uint32_t gone = (missing >> (2 * stage)) & 3u;
+    const bool masked = gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min;
+    bool moved = false;
+    uint32_t pf[2][NT][2];              // p as fp16 pairs of columns: tokens g, g + 8
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& v = s[u][j][k];
+          v *= fac[j][k & 1];
+          if (masked) {
+            const int t = tile * kTile + 16 * u + 8 * (k >> 1) + g;
+            if (t < c_lo[j][k & 1] || t >= c_hi[j][k & 1] || ((gone >> u) & 1u)) v = -INFINITY;
+          }
+          top[k & 1] = fmaxf(top[k & 1], v);
+        }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], d));
+        moved = moved || top[c] > m[j][c];
+        top[c] = fmaxf(top[c], m[j][c]);
+      }
+      const float base0 = top[0] == -INFINITY ? 0.0f : top[0], base1 = top[1] == -INFINITY ? 0.0f : top[1];
+      const float f0 = ex2(m[j][0] - base0), f1 = ex2(m[j][1] - base1);
+      m[j][0] = top[0];
+      m[j][1] = top[1];
+      float add[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[u][j][k] = ex2(s[u][j][k] - ((k & 1) ? base1 : base0));
+          add[k & 1] += s[u][j][k];
+        }
+        pf[u][j][0] = pack_f16x2(s[u][j][0], s[u][j][1]);
+        pf[u][j][1] = pack_f16x2(s[u][j][2], s[u][j][3]);
+      }
+      l[j][0] = fmaf(l[j][0], f0, add[0]);
+      l[j][1] = fmaf(l[j][1], f1, add[1]);
+      if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d) {
+          o[j][d][0] *= f0; o[j][d][1] *= f1; o[j][d][2] *= f0; o[j][d][3] *= f1;
+        }
+      }
+    }
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t pb[NT][2];               // B operand: row g's tokens 2q, 2q + 1 and 2q + 8, 2q + 9
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        pb[j][0] = movm_t(pf[u][j][0]);
+        pb[j][1] = movm_t(pf[u][j][1]);
+      }
+      uint32_t vw[2][4];                // [tokens 0 .. 7 or 8 .. 15][block]
+      if (NB == 4) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) ldsm_t(vw[hf], base + kCodes + tile_at<D>(16 * u + 8 * hf + (lane & 7), lane >> 3));
+      } else {
+        uint32_t r[4];
+        ldsm_t(r, base + kCodes + tile_at<D>(16 * u + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+        vw[0][0] = r[0]; vw[0][1] = r[1]; vw[1][0] = r[2]; vw[1][1] = r[3];
+      }
+      uint32_t vs[2][4];                // scales of tokens (2q, 2q + 1) + 8 hf as fp16 pairs, per 32-block
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* sp = gen + 2 * kCodes + kScales + (16 * u + 8 * hf + 2 * q) * kv::scale_bytes(D);
+        uint32_t t0[2], t1[2];
+        if (NB == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(sp);
+          t0[0] = v.x; t0[1] = v.y; t1[0] = v.z; t1[1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(sp);
+          t0[0] = t0[1] = v.x;
+          t1[0] = t1[1] = v.y;
+        }
+#pragma unroll
+        for (int pr = 0; pr < NB / 2; ++pr) {
+          if (FMT == WQ_Q4_0) {
+            vs[hf][2 * pr] = __byte_perm(t0[pr], t1[pr], 0x5410u);
+            vs[hf][2 * pr + 1] = __byte_perm(t0[pr], t1[pr], 0x7632u);
+          } else {
+            // four codes of lane g lie in the 16-block g >> 2 of the 32 elements
+            e4m3_pairs(__byte_perm(t0[pr], t1[pr], (g >> 2) ? 0x7351u : 0x6240u), vs[hf][2 * pr], vs[hf][2 * pr + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        uint32_t av[2][4];              // [tokens][element 4g + e of the block]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t w = vw[hf][blk];
+          if (FMT == WQ_Q4_0) {
+            signed_pairs(w, av[hf][0], av[hf][1]);
+            signed_pairs(w >> 8, av[hf][2], av[hf][3]);
+          } else {
+            // bytes (token 2q in the low nibble, 2q + 1 in the high): elements 0, 2, 1, 3
+            const uint32_t ev = (w & 0x0F0Fu) | ((w >> 12) & 0xF0F0u), od = ((w >> 4) & 0x0F0Fu) | ((w >> 16) & 0xF0F0u);
+            uint32_t r[4];
+            e2m1_pairs(__byte_perm(ev, od, 0x5410u), r);
+            av[hf][0] = mul2(r[0], vs[hf][blk]);
+            av[hf][2] = mul2(r[1], vs[hf][blk]);
+            av[hf][1] = mul2(r[2], vs[hf][blk]);
+            av[hf][3] = mul2(r[3], vs[hf][blk]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t b0 = pb[j][0], b1 = pb[j][1];
+          if (FMT == WQ_Q4_0) {
+            b0 = mul2(b0, vs[0][blk]);
+            b1 = mul2(b1, vs[1][blk]);
+            if (masked) {               // a weight of zero takes nothing from a scale that is no number
+              b0 = ((pb[j][0] & 0x7FFFu) ? b0 & 0xFFFFu : 0u) | ((pb[j][0] & 0x7FFF0000u) ? b0 & 0xFFFF0000u : 0u);
+              b1 = ((pb[j][1] & 0x7FFFu) ? b1 & 0xFFFFu : 0u) | ((pb[j][1] & 0x7FFF0000u) ? b1 & 0xFFFF0000u : 0u);
+            }
+          }
+          mma(o[j][2 * blk], av[0][0], av[0][1], av[1][0], av[1][1], b0, b1);
+          mma(o[j][2 * blk + 1], av[0][2], av[0][3], av[1][2], av[1][3], b0, b1);
+        }
+      }
+    }
+    if (++stage == kStages) stage = 0;
+    __syncwarp();                       // every lane has read the stage before it is filled again
+  }
+  cp_wait<0>();
+
+  // ---------------------------------------------------------------- joining the warps
+  // o[j][2 blk + e2]: c[0], c[1]: element 32 blk + 4 g + 2 e2 of rows 2q, 2q + 1; c[2], c[3]: the next one
+  const float vg = FMT == WQ_NVFP4 && a.kv.g[1] ? *a.kv.g[1] : 1.0f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], d);
+  __syncthreads();                      // the rings are free
+  float* so = reinterpret_cast<float*>(smem);
+  float2* sml = reinterpret_cast<float2*>(smem + kWarps * 8 * NT * D * 4);
+  if (g == 0) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) sml[warp * 8 * NT + 8 * j + 2 * q + c] = make_float2(m[j][c], l[j][c]);
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = FMT == WQ_NVFP4 ? o[j][2 * blk + e2][k] * vg : o[j][2 * blk + e2][k];
+        float* dst = so + (warp * 8 * NT + 8 * j + 2 * q) * D + 32 * blk + 4 * g + 2 * e2;
+        *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[2]);
+        *reinterpret_cast<float2*>(dst + D) = make_float2(v[1], v[3]);
+      }
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = -INFINITY, sum = 0.0f, out = 0.0f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
+  constexpr int kPerRow = 32 * kWarps / (8 * NT) > 0 ? 32 * kWarps / (8 * NT) : 1;   // threads per row
+  const int row = threadIdx.x / kPerRow, part = threadIdx.x % kPerRow;
+  float top = -INFINITY, sum = 0.0f, f[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * 8 * NT + row].x);
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const float f = sl[w] == 0.0f ? 0.0f : exp2f(sm[w] - top);
-    sum = fmaf(sl[w], f, sum);
-    out = fmaf(so[w][threadIdx.x], f, out);
+    const float2 v = sml[w * 8 * NT + row];
+    f[w] = v.y == 0.0f ? 0.0f : ex2(v.x - top);
+    sum = fmaf(v.y, f[w], sum);
   }
-  out = sum == 0.0f ? 0.0f : out / sum;
-  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head + threadIdx.x;
-  if (a.f32) reinterpret_cast<float*>(a.out.p)[at] = out;
-  else reinterpret_cast<__nv_bfloat16*>(a.out.p)[at] = __float2bfloat16_rn(out);
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(b * a.tokens + i) * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  const int64_t r = r0 + row, i = r / p.group;
+  const int hq = h * p.group + (int)(r - i * p.group);
+  if (p.splits > 1) {
+    const int64_t slot = (tile_id * p.splits + split) * 8 * NT + row;
+    if (part == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
+#pragma unroll 4
+    for (int d = part; d < D; d += kPerRow) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], so[(w * 8 * NT + row) * D + d], v);
+      p.part_o[slot * D + d] = v;
+    }
+  } else if (i < a.tokens) {
+    const bool some = r < rows && sum != 0.0f;
+    const float inv = some ? 1.0f / sum : 0.0f;
+    const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head;
+#pragma unroll 4
+    for (int d = part; d < D; d += kPerRow) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], so[(w * 8 * NT + row) * D + d], v);
+      put(a, at + d, some ? v * inv : 0.0f);
+    }
+    if (a.lse && part == 0) a.lse[(b * a.tokens + i) * a.q_heads + hq] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  }
 }
 
-template <int FMT, int D>
-int attend_t(const AttendArgs& a, cudaStream_t s) {
-  attend_kernel<FMT, D><<<dim3((unsigned)(a.batch * a.tokens), (unsigned)a.q_heads), 32 * kWarps, 0, s>>>(a);
+// Joins the splits of a row: one warp per query row and head, lanes over the elements.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tile_rows) {
+  const AttendArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // (sequence, token, head)
+  if (id >= a.batch * a.tokens * a.q_heads) return;
+  const int64_t bi = id / a.q_heads, b = bi / a.tokens, i = bi - b * a.tokens;
+  const int hq = (int)(id - bi * a.q_heads), h = hq / p.group;
+  const int64_t r = i * p.group + (hq - h * p.group);
+  const bool valid = i < kv::count_of(a.counts, b, a.tokens);
+  const int64_t slot = ((b * a.kv.heads + h) * p.row_tiles + r / tile_rows) * p.splits * tile_rows + r % tile_rows;
+  float top = -INFINITY, sum = 0.0f, o[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+  for (int s = 0; valid && s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot + (int64_t)s * tile_rows));
+    top = fmaxf(top, ml.x);
+  }
+#pragma unroll 4
+  for (int s = 0; valid && s < p.splits; ++s) {
+    const int64_t at = slot + (int64_t)s * tile_rows;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+    const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, p.part_o[at * D + 32 * e + lane], o[e]);
+  }
+  const bool some = sum != 0.0f;
+  const float inv = some ? 1.0f / sum : 0.0f;
+  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) put(a, at + 32 * e + lane, some ? o[e] * inv : 0.0f);
+  if (a.lse && lane == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+struct Plan {
+  int nt, row_tiles, splits;
+  size_t slots;      // partial rows in the workspace
+};
+
+Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, int64_t window) {
+  Plan pl{};
+  const int64_t group = q_heads / kv.heads, rows = tokens * group;
+  pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  pl.row_tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+  const int64_t blocks = batch * kv.heads * pl.row_tiles;
+  int64_t seen = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
+  if (window > 0 && window + tokens < seen) seen = window + tokens;
+  const int64_t tiles = (seen + kTile - 1) / kTile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
+  const int64_t want = (int64_t)kSms * (pl.nt == 1 ? 4 : 2) / (blocks > 0 ? blocks : 1);
+  pl.splits = (int)(want < 1 ? 1 : want > most ? (most < 1 ? 1 : most) : want);
+  pl.slots = pl.splits > 1 ? (size_t)(blocks * pl.splits * 8 * pl.nt) : 0;
+  return pl;
+}
+
+template <int FMT, int D, int NT>
+int launch(const Params& p, cudaStream_t s) {
+  static cudaError_t attr = cudaFuncSetAttribute(attend_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 smem_bytes(D, NT));
+  if (attr != cudaSuccess) return WQ_ERR_CUDA;
+  const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.splits;
+  if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  attend_kernel<FMT, D, NT><<<(unsigned)grid, 32 * kWarps, smem_bytes(D, NT), s>>>(p);
   count_launch();
+  if (p.splits > 1) {
+    const int64_t warps = p.a.batch * p.a.tokens * p.a.q_heads;
+    join_kernel<D><<<(unsigned)((warps + 3) / 4), 128, 0, s>>>(p, 8 * NT);
+    count_launch();
+  }
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
+template <int FMT, int D>
+int launch_nt(const Params& p, int nt, cudaStream_t s) {
+  return nt == 1 ? launch<FMT, D, 1>(p, s) : nt == 2 ? launch<FMT, D, 2>(p, s) : launch<FMT, D, 4>(p, s);
 }
 
 }  // namespace
 
-size_t attend_workspace(const KvArgs&, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len) {
+  return plan(kv, batch, tokens, q_heads, max_len, 0).slots * ((size_t)kv.dim + 2) * sizeof(float);
+}
 
 int attend(const AttendArgs& a, cudaStream_t s) {
-  if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? attend_t<WQ_Q4_0, 64>(a, s) : attend_t<WQ_Q4_0, 128>(a, s);
-  return a.kv.dim == 64 ? attend_t<WQ_NVFP4, 64>(a, s) : attend_t<WQ_NVFP4, 128>(a, s);
+  const Plan pl = plan(a.kv, a.batch, a.tokens, a.q_heads, a.max_len, a.window);
+  Params p{};
+  p.a = a;
+  p.group = (int)(a.q_heads / a.kv.heads);
+  p.row_tiles = pl.row_tiles;
+  p.splits = pl.splits;
+  p.part_o = reinterpret_cast<float*>(a.workspace);
+  p.part_ml = p.part_o + pl.slots * a.kv.dim;
+  if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? launch_nt<WQ_Q4_0, 64>(p, pl.nt, s) : launch_nt<WQ_Q4_0, 128>(p, pl.nt, s);
+  return a.kv.dim == 64 ? launch_nt<WQ_NVFP4, 64>(p, pl.nt, s) : launch_nt<WQ_NVFP4, 128>(p, pl.nt, s);
 }
 
 int take_status_attend() {
