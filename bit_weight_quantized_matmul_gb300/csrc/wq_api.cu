@@ -168,6 +168,10 @@ int check_cache(const wq_kv_cache* c, KvArgs& a) {
   a.table_ld = c->table_ld;
   a.pages = c->pages;
   a.page_size = (int32_t)c->page_size;
+  int log = 4;  // page_size <= 2^log; the rounded-up multiplier's error times t stays below 2^(31 + log)
+  while ((int64_t(1) << log) < c->page_size) ++log;
+  a.page_mul = (uint32_t)((uint64_t(1) << (31 + log)) / (uint64_t)c->page_size + (c->page_size == (int64_t(1) << log) ? 0 : 1));
+  a.page_shift = (uint32_t)(log - 1);
   a.fmt = c->fmt;
   a.heads = c->heads;
   a.dim = c->dim;

@@ -21,6 +21,8 @@
 // Q is scaled per row by a power of two, so that its bf16 values are exact in fp16.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "wq_kv.cuh"
 
 namespace wq {
@@ -46,9 +48,10 @@ struct Params {
   AttendArgs a;
   int group;        // query heads per cached head
   int row_tiles;    // blocks of 8 * NT query rows per cached head
-  int splits;       // blocks that share the tokens of one row tile
-  float* part_o;    // [row tile][split][8 * NT][D] unnormalised outputs
-  float* part_ml;   // [row tile][split][8 * NT][2] their m (base 2) and l
+  int cluster;      // blocks of a cluster, which share a range of the tokens of one row tile
+  int parts;        // clusters that share the tokens of one row tile
+  float* part_o;    // [row tile][part][8 * NT][D] unnormalised outputs
+  float* part_ml;   // [row tile][part][8 * NT][2] their m (base 2) and l
 };
 
 // Byte offset of 16-byte chunk `col` (a block of 32 codes) of token `row` in a tile: the chunks of
@@ -88,6 +91,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A B + C with C kept.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -119,16 +129,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Four bytes of two E2M1 codes -> four fp16 pairs (low nibble in the low half).
-__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
-}
 // Four E4M3 bytes -> two fp16 pairs.
 __device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 h0, h1;\n\t"
@@ -150,6 +150,15 @@ __device__ __forceinline__ void put(const AttendArgs& a, int64_t at, float v) {
   else reinterpret_cast<__nv_bfloat16*>(a.out.p)[at] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void put4(const AttendArgs& a, int64_t at, float4 v) {
+  if (a.f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out.p) + at) = v;
+  else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out.p) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void ld_shared_cluster_f32x4(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
+}
+
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(const __grid_constant__ Params p) {
   constexpr int NB = D / 32;            // 32-element blocks of a row
@@ -160,8 +169,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
 
   uint32_t x = blockIdx.x;
-  const int split = x % p.splits;
-  x /= p.splits;
+  const int splits = p.cluster * p.parts;
+  const int split = x % splits;         // the blocks of a cluster are neighbours
+  x /= splits;
   const int64_t tile_id = x;            // (sequence, cached head, row tile)
   const int rt = x % p.row_tiles;
   x /= p.row_tiles;
@@ -185,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   const int lo_max = any ? lo_of(i_last) : 0, hi_min = any ? hi_of(i_first) : 0;
   const int tile0 = lo_min / kTile;
   const int ntiles = hi_max > lo_min ? (hi_max + kTile - 1) / kTile - tile0 : 0;
-  const int per = (ntiles + p.splits - 1) / p.splits;
+  const int per = (ntiles + splits - 1) / splits;
   const int t_end = tile0 + min(ntiles, (split + 1) * per);
   const int t_begin = tile0 + min(ntiles, split * per) + warp;
 
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     int64_t page = b;
     int off = t;
     if (a.kv.table) {
-      const int pg = (unsigned)t / (unsigned)a.kv.page_size;
+      const int pg = kv::page_of(a.kv, t);
       off = t - pg * a.kv.page_size;
       page = a.kv.table[b * a.kv.table_ld + pg];
     }
@@ -215,18 +225,24 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     const int64_t row[2] = {__shfl_sync(0xFFFFFFFFu, mine, 0), __shfl_sync(0xFFFFFFFFu, mine, 1)};
     missing = (missing & ~(3u << (2 * stage))) | ((row[0] == -2 ? 1u : 0u) | (row[1] == -2 ? 2u : 0u)) << (2 * stage);
     const uint32_t dst = ring + stage * stage_bytes(D);
-    constexpr int kPer = kTile * NB / 32;            // 16-byte chunks per lane
+    // A half's rows are contiguous: lane l copies bytes 16 l .. 16 l + 15 of every 512.
+    const uint32_t to = dst + tile_at<D>(lane / NB, lane % NB);
+    const int64_t own = (lane >> 4) ? row[1] : row[0];
+    const bool whole = row[0] >= 0 && row[1] >= 0 && (tile + 1) * kTile <= hi_max;
+    constexpr int kPer = D / 64;        // 512-byte pieces of a half
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int c = j * 32 + lane, r = c / NB, col = c % NB, half = r >> 4;
-      const bool in = row[half] >= 0 && tile * kTile + r < hi_max;
-      const int64_t at = in ? (row[half] + (r & 15)) * (D / 2) + col * 16 : 0;
-      cp16(dst + tile_at<D>(r, col), a.kv.codes[0] + at, in ? 16 : 0);
-      cp16(dst + kCodes + tile_at<D>(r, col), a.kv.codes[1] + at, in ? 16 : 0);
+    for (int half = 0; half < 2; ++half) {
+      const int64_t at = row[half] * (D / 2) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int r = 16 * half + (512 * j + 16 * lane) / (D / 2);
+        const bool in = whole || (row[half] >= 0 && tile * kTile + r < hi_max);
+        cp16(to + (half * kPer + j) * 512, a.kv.codes[0] + (in ? at + 512 * j : 0), in ? 16 : 0);
+        cp16(to + kCodes + (half * kPer + j) * 512, a.kv.codes[1] + (in ? at + 512 * j : 0), in ? 16 : 0);
+      }
     }
-    const int half = lane >> 4;
-    const bool in = (half ? row[1] : row[0]) >= 0 && tile * kTile + lane < hi_max;
-    const int64_t at = in ? ((half ? row[1] : row[0]) + (lane & 15)) * kv::scale_bytes(D) : 0;
+    const bool in = whole || (own >= 0 && tile * kTile + lane < hi_max);
+    const int64_t at = in ? (own + (lane & 15)) * kv::scale_bytes(D) : 0;
     cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + lane * kv::scale_bytes(D), a.kv.scales[0] + at,
                                  in ? kv::scale_bytes(D) : 0);
     cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + kScales + lane * kv::scale_bytes(D), a.kv.scales[1] + at,
@@ -325,21 +341,11 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   }
 
   // ---------------------------------------------------------------- tiles
-  int stage = 0;
-  for (int tile = t_begin; tile < t_end; tile += kWarps) {
-    {
-      const int ahead = tile + (kStages - 1) * kWarps;
-      int s = stage + kStages - 1;
-      if (s >= kStages) s -= kStages;
-      if (ahead < t_end) issue(ahead, s, next);
-      cp_commit();
-      next = locate(ahead + kWarps);
-    }
-    cp_wait<kStages - 1>();
-    __syncwarp();
+  // One tile; MASKED: some row does not see all of it.
+  auto work = [&](auto masked_c, int tile, int stage, uint32_t gone) {
+    constexpr bool masked = decltype(masked_c)::value;
     const uint32_t base = ring + stage * stage_bytes(D);
     const uint8_t* gen = smem + (base - smem_u32(smem));
-
     // ---- scores of 2 x 16 tokens
     float s[2][NT][4];
 #pragma unroll
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
             av[u][hf][2] = (w >> 8) & 0x000F000Fu;
             av[u][hf][3] = (w >> 8) & 0x00F000F0u;
           } else {
-            e2m1_pairs(w, av[u][hf]);
+            kv::e2m1_pairs(w, av[u][hf]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) av[u][hf][e] = mul2(av[u][hf][e], ks[u][hf][FMT == WQ_NVFP4 ? blk : 0]);
           }
@@ -417,8 +423,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
         for (int u = 0; u < 2; ++u) {
           if (FMT == WQ_Q4_0) {
             const int ib = FMT == WQ_Q4_0 ? blk : 0;
-            float c[4] = {init[j][ib][0], init[j][ib][1], init[j][ib][0], init[j][ib][1]};
-            mma(c, av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1]);
+            float c[4];
+            mma_from(c, av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1], init[j][ib][0], init[j][ib][1]);
             mma(c, av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[u][j][k] = fmaf(kd[u][k >> 1][ib], c[k], s[u][j][k]);
@@ -431,8 +437,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     }
 
     // ---- online softmax: c[0], c[1] are token g's columns 2q, 2q + 1, c[2], c[3] token g + 8's
-    const uint32_t gone = (missing >> (2 * stage)) & 3u;
-    const bool masked = gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min;
     bool moved = false;
     uint32_t pf[2][NT][2];              // p as fp16 pairs of columns: tokens g, g + 8
 #pragma unroll
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
             // bytes (token 2q in the low nibble, 2q + 1 in the high): elements 0, 2, 1, 3
             const uint32_t ev = (w & 0x0F0Fu) | ((w >> 12) & 0xF0F0u), od = ((w >> 4) & 0x0F0Fu) | ((w >> 16) & 0xF0F0u);
             uint32_t r[4];
-            e2m1_pairs(__byte_perm(ev, od, 0x5410u), r);
+            kv::e2m1_pairs(__byte_perm(ev, od, 0x5410u), r);
             av[hf][0] = mul2(r[0], vs[hf][blk]);
             av[hf][2] = mul2(r[1], vs[hf][blk]);
             av[hf][1] = mul2(r[2], vs[hf][blk]);
@@ -560,6 +564,22 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
         }
       }
     }
+  };
+  int stage = 0;
+  for (int tile = t_begin; tile < t_end; tile += kWarps) {
+    {
+      const int ahead = tile + (kStages - 1) * kWarps;
+      int s = stage + kStages - 1;
+      if (s >= kStages) s -= kStages;
+      if (ahead < t_end) issue(ahead, s, next);
+      cp_commit();
+      next = locate(ahead + kWarps);
+    }
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t gone = (missing >> (2 * stage)) & 3u;
+    if (gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min) work(std::true_type{}, tile, stage, gone);
+    else work(std::false_type{}, tile, stage, 0u);
     if (++stage == kStages) stage = 0;
     __syncwarp();                       // every lane has read the stage before it is filled again
   }
@@ -597,65 +617,130 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
         *reinterpret_cast<float2*>(dst + D) = make_float2(v[1], v[3]);
       }
   __syncthreads();
-  constexpr int kPerRow = 32 * kWarps / (8 * NT) > 0 ? 32 * kWarps / (8 * NT) : 1;   // threads per row
+  // Thread t of a row's kPerRow takes its elements 4 t, 4 t + 4 kPerRow, ...
+  constexpr int kRows = 8 * NT, kPerRow = 32 * kWarps / kRows;
   const int row = threadIdx.x / kPerRow, part = threadIdx.x % kPerRow;
   float top = -INFINITY, sum = 0.0f, f[kWarps];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * 8 * NT + row].x);
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * kRows + row].x);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const float2 v = sml[w * 8 * NT + row];
+    const float2 v = sml[w * kRows + row];
     f[w] = v.y == 0.0f ? 0.0f : ex2(v.x - top);
     sum = fmaf(v.y, f[w], sum);
   }
-  const int64_t r = r0 + row, i = r / p.group;
-  const int hq = h * p.group + (int)(r - i * p.group);
-  if (p.splits > 1) {
-    const int64_t slot = (tile_id * p.splits + split) * 8 * NT + row;
-    if (part == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
-#pragma unroll 4
-    for (int d = part; d < D; d += kPerRow) {
-      float v = 0.0f;
+  float4 acc[D / (4 * kPerRow)];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], so[(w * 8 * NT + row) * D + d], v);
-      p.part_o[slot * D + d] = v;
+  for (int k = 0; k < D / (4 * kPerRow); ++k) {
+    acc[k] = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + 4 * (part + k * kPerRow));
+      acc[k].x = fmaf(f[w], v.x, acc[k].x);
+      acc[k].y = fmaf(f[w], v.y, acc[k].y);
+      acc[k].z = fmaf(f[w], v.z, acc[k].z);
+      acc[k].w = fmaf(f[w], v.w, acc[k].w);
+    }
+  }
+
+  // ---------------------------------------------------------------- joining the blocks of a cluster
+  // Each leaves its O, m and l in its own shared memory (warp 0's part), and takes every cluster'th
+  // vector of the joined rows.
+  int first = 0, step = 1;
+  if (p.cluster > 1) {
+    first = (int)cluster_ctarank();
+    step = p.cluster;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < D / (4 * kPerRow); ++k) *reinterpret_cast<float4*>(so + row * D + 4 * (part + k * kPerRow)) = acc[k];
+    if (part == 0) sml[row] = make_float2(top, sum);
+    cluster_sync();
+    float2 ml[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.0f);
+      if (c < p.cluster) {
+        const uint32_t at = map_shared_rank(smem_u32(sml + row), c);
+        ml[c] = make_float2(ld_shared_cluster_f32(at), ld_shared_cluster_f32(at + 4));
+      }
+    }
+    top = -INFINITY;
+    sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) top = fmaxf(top, ml[c].x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ml[c].x = ml[c].y == 0.0f ? 0.0f : ex2(ml[c].x - top);
+      sum = fmaf(ml[c].y, ml[c].x, sum);
+    }
+#pragma unroll
+    for (int k = 0; k < D / (4 * kPerRow); ++k) {
+      const int vec = part + k * kPerRow;
+      if (vec % step != first) continue;
+      acc[k] = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c < p.cluster) {
+          float v[4];
+          ld_shared_cluster_f32x4(map_shared_rank(smem_u32(so + row * D + 4 * vec), c), v);
+          acc[k].x = fmaf(ml[c].x, v[0], acc[k].x);
+          acc[k].y = fmaf(ml[c].x, v[1], acc[k].y);
+          acc[k].z = fmaf(ml[c].x, v[2], acc[k].z);
+          acc[k].w = fmaf(ml[c].x, v[3], acc[k].w);
+        }
+      }
+    }
+  }
+
+  const int64_t r = r0 + row, i = r / p.group;
+  if (p.parts > 1) {
+    const int64_t slot = (tile_id * p.parts + split / p.cluster) * kRows + row;
+    if (part == 0 && first == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
+#pragma unroll
+    for (int k = 0; k < D / (4 * kPerRow); ++k) {
+      const int vec = part + k * kPerRow;
+      if (vec % step == first) *reinterpret_cast<float4*>(p.part_o + slot * D + 4 * vec) = acc[k];
     }
   } else if (i < a.tokens) {
+    const int hq = h * p.group + (int)(r - i * p.group);
     const bool some = r < rows && sum != 0.0f;
     const float inv = some ? 1.0f / sum : 0.0f;
     const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head;
-#pragma unroll 4
-    for (int d = part; d < D; d += kPerRow) {
-      float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], so[(w * 8 * NT + row) * D + d], v);
-      put(a, at + d, some ? v * inv : 0.0f);
+    for (int k = 0; k < D / (4 * kPerRow); ++k) {
+      const int vec = part + k * kPerRow;
+      if (vec % step != first) continue;
+      if (some) acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+      else acc[k] = make_float4(0, 0, 0, 0);
+      put4(a, at + 4 * vec, acc[k]);
     }
-    if (a.lse && part == 0) a.lse[(b * a.tokens + i) * a.q_heads + hq] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (a.lse && part == 0 && first == 0)
+      a.lse[(b * a.tokens + i) * a.q_heads + hq] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
   }
+  if (p.cluster > 1) cluster_sync();    // the others may still read this block's shared memory
 }
 
-// Joins the splits of a row: one warp per query row and head, lanes over the elements.
+// Joins the parts of a query row and head: a block per row, its warps over the parts, lanes over
+// the elements, then the warps in order.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tile_rows) {
   const AttendArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // (sequence, token, head)
-  if (id >= a.batch * a.tokens * a.q_heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t id = blockIdx.x;        // (sequence, token, head)
   const int64_t bi = id / a.q_heads, b = bi / a.tokens, i = bi - b * a.tokens;
   const int hq = (int)(id - bi * a.q_heads), h = hq / p.group;
   const int64_t r = i * p.group + (hq - h * p.group);
-  const bool valid = i < kv::count_of(a.counts, b, a.tokens);
-  const int64_t slot = ((b * a.kv.heads + h) * p.row_tiles + r / tile_rows) * p.splits * tile_rows + r % tile_rows;
+  const int parts = i < kv::count_of(a.counts, b, a.tokens) ? p.parts : 0;
+  const int64_t slot = ((b * a.kv.heads + h) * p.row_tiles + r / tile_rows) * p.parts * tile_rows + r % tile_rows;
+  __shared__ float so[4][D], sl[4];
   float top = -INFINITY, sum = 0.0f, o[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
-  for (int s = 0; valid && s < p.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot + (int64_t)s * tile_rows));
-    top = fmaxf(top, ml.x);
-  }
+  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_ml[2 * (slot + (int64_t)s * tile_rows)]);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll 4
-  for (int s = 0; valid && s < p.splits; ++s) {
+  for (int s = warp; s < parts; s += 4) {
     const int64_t at = slot + (int64_t)s * tile_rows;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
     const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
@@ -663,16 +748,21 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, p.part_o[at * D + 32 * e + lane], o[e]);
   }
-  const bool some = sum != 0.0f;
-  const float inv = some ? 1.0f / sum : 0.0f;
-  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head;
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) put(a, at + 32 * e + lane, some ? o[e] * inv : 0.0f);
-  if (a.lse && lane == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  for (int e = 0; e < D / 32; ++e) so[warp][32 * e + lane] = o[e];
+  if (lane == 0) sl[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const bool some = sum != 0.0f;
+  const float v = (so[0][threadIdx.x] + so[1][threadIdx.x]) + (so[2][threadIdx.x] + so[3][threadIdx.x]);
+  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head + threadIdx.x;
+  put(a, at, some ? v * (1.0f / sum) : 0.0f);
+  if (a.lse && threadIdx.x == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 struct Plan {
-  int nt, row_tiles, splits;
+  int nt, row_tiles, cluster, parts;
   size_t slots;      // partial rows in the workspace
 };
 
@@ -685,9 +775,11 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   int64_t seen = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
   if (window > 0 && window + tokens < seen) seen = window + tokens;
   const int64_t tiles = (seen + kTile - 1) / kTile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
-  const int64_t want = (int64_t)kSms * (pl.nt == 1 ? 4 : 2) / (blocks > 0 ? blocks : 1);
-  pl.splits = (int)(want < 1 ? 1 : want > most ? (most < 1 ? 1 : most) : want);
-  pl.slots = pl.splits > 1 ? (size_t)(blocks * pl.splits * 8 * pl.nt) : 0;
+  int64_t want = (int64_t)kSms * (pl.nt == 1 ? 4 : 2) / (blocks > 0 ? blocks : 1);
+  if (want > most) want = most;
+  pl.cluster = want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
+  pl.parts = (int)(want / pl.cluster < 1 ? 1 : want / pl.cluster);
+  pl.slots = pl.parts > 1 ? (size_t)(blocks * pl.parts * 8 * pl.nt) : 0;
   return pl;
 }
 
@@ -696,13 +788,23 @@ int launch(const Params& p, cudaStream_t s) {
   static cudaError_t attr = cudaFuncSetAttribute(attend_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem_bytes(D, NT));
   if (attr != cudaSuccess) return WQ_ERR_CUDA;
-  const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.splits;
+  const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.cluster * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
-  attend_kernel<FMT, D, NT><<<(unsigned)grid, 32 * kWarps, smem_bytes(D, NT), s>>>(p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem_bytes(D, NT);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, attend_kernel<FMT, D, NT>, p) != cudaSuccess) return WQ_ERR_CUDA;
   count_launch();
-  if (p.splits > 1) {
-    const int64_t warps = p.a.batch * p.a.tokens * p.a.q_heads;
-    join_kernel<D><<<(unsigned)((warps + 3) / 4), 128, 0, s>>>(p, 8 * NT);
+  if (p.parts > 1) {
+    join_kernel<D><<<(unsigned)(p.a.batch * p.a.tokens * p.a.q_heads), 128, 0, s>>>(p, 8 * NT);
     count_launch();
   }
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
@@ -724,7 +826,8 @@ int attend(const AttendArgs& a, cudaStream_t s) {
   p.a = a;
   p.group = (int)(a.q_heads / a.kv.heads);
   p.row_tiles = pl.row_tiles;
-  p.splits = pl.splits;
+  p.cluster = pl.cluster;
+  p.parts = pl.parts;
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = p.part_o + pl.slots * a.kv.dim;
   if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? launch_nt<WQ_Q4_0, 64>(p, pl.nt, s) : launch_nt<WQ_Q4_0, 128>(p, pl.nt, s);

@@ -117,6 +117,7 @@ struct KvArgs {
   int64_t pages;
   int64_t capacity;     // tokens per sequence
   int32_t page_size, fmt, heads, dim;
+  uint32_t page_mul, page_shift;  // t / page_size = umulhi(t, page_mul) >> page_shift for 0 <= t < 2^31
 };
 struct HeadsArg {
   void* p;

@@ -14,15 +14,30 @@ namespace kv {
 // Scale bytes of one row of D elements: q4_0 an fp16 per 32, NVFP4 an E4M3 byte per 16 (equal).
 constexpr int scale_bytes(int D) { return D / 16; }
 
-// Row (of the [pages, heads, page_size] rows) of position t >= 0 of sequence b and head h, or -1 (and
+__device__ __forceinline__ int page_of(const KvArgs& kv, int t) {
+  return (int)(__umulhi((uint32_t)t, kv.page_mul) >> kv.page_shift);
+}
+
+// Four bytes of two E2M1 codes -> four fp16 pairs (low nibble in the low half), exact.
+__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+
+// Row (of the [pages, heads, page_size] rows) of position t of sequence b and head h, or -1 (and
 // WQ_ERR_ARG in the status word) where the position or its table entry lies outside the cache.
-__device__ __forceinline__ int64_t row_of(const KvArgs& kv, int64_t b, int t, int h) {
+__device__ __forceinline__ int64_t row_of(const KvArgs& kv, int64_t b, int64_t t, int h) {
   int64_t page = b;
-  int off = t;
-  bool ok = t < kv.capacity;
+  int off = (int)t;
+  bool ok = t >= 0 && t < kv.capacity;
   if (kv.table && ok) {
-    const int p = t / kv.page_size;
-    off = t - p * kv.page_size;
+    const int p = page_of(kv, off);
+    off -= p * kv.page_size;
     page = kv.table[b * kv.table_ld + p];
   }
   ok = ok && page >= 0 && page < kv.pages;
@@ -43,11 +58,17 @@ __device__ __forceinline__ int count_of(const int32_t* counts, int64_t b, int64_
 // NVFP4: (E2M1(c) * s) * g, the inner product exact.
 template <int FMT>
 __device__ __forceinline__ void decode8(uint32_t w, float s, float g, float (&v)[8]) {
+  if (FMT == WQ_Q4_0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = (w >> (4 * i)) & 15u;
-    if (FMT == WQ_Q4_0) v[i] = __fmul_rn((float)((int)c - 8), s);
-    else v[i] = __fmul_rn(__fmul_rn(kE2M1[c], s), g);
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn((float)((int)((w >> (4 * i)) & 15u) - 8), s);
+  } else {
+    uint32_t r[4];
+    e2m1_pairs(w, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __fmul_rn(__fmul_rn(f16_bits_to_f32(r[i] & 0xFFFFu), s), g);
+      v[2 * i + 1] = __fmul_rn(__fmul_rn(f16_bits_to_f32(r[i] >> 16), s), g);
+    }
   }
 }
 // Scale of element e of the row whose scale bytes start at p.

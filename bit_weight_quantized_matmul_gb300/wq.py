@@ -9,6 +9,7 @@ pass raw device pointers plus the current CUDA stream.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -116,8 +117,12 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The raw handle of `stream`, or of the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _fmt(fmt):
@@ -285,16 +290,21 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
     return KVCache(fmt, codes[0], scales[0], codes[1], scales[1], table, k_g, v_g)
 
 
+_pack_heads = struct.Struct("Pqqq").pack
+
+
 def _heads(t, dtype):
-    """[batch, token, head, dim] view -> wq_heads (dim contiguous; other strides as they are)."""
-    assert t.is_cuda and t.dtype == dtype and t.stride(3) == 1
-    s = t.stride()
-    return wq_heads(t.data_ptr(), s[0], s[1], s[2])
+    """[batch, token, head, dim] view -> the bytes of a wq_heads (dim contiguous; other strides as they are)."""
+    sb, st, sh, sd = t.stride()
+    assert t.is_cuda and t.dtype is dtype and sd == 1
+    return _pack_heads(t.data_ptr(), sb, st, sh)
 
 
 def _index(t, batch):
-    assert t is None or (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and t.numel() == batch)
-    return None if t is None else t.data_ptr()
+    if t is None:
+        return None
+    assert t.is_cuda and t.dtype is torch.int32 and t.is_contiguous() and t.numel() == batch
+    return t.data_ptr()
 
 
 def kv_append(cache, k, v, start=None, counts=None, stream=None):
@@ -302,8 +312,8 @@ def kv_append(cache, k, v, start=None, counts=None, stream=None):
     of the cache (int32 CUDA tensors; None: 0, and all tokens)."""
     batch, tokens, heads, dim = k.shape
     assert v.shape == k.shape and heads == cache.heads and dim == cache.dim and batch <= cache.batch
-    _check("wq_kv_append", lib.wq_kv_append(cache.ref, ctypes.byref(_heads(k, torch.bfloat16)),
-                                            ctypes.byref(_heads(v, torch.bfloat16)), batch, tokens,
+    _check("wq_kv_append", lib.wq_kv_append(cache.ref, _heads(k, torch.bfloat16),
+                                            _heads(v, torch.bfloat16), batch, tokens,
                                             _index(start, batch), _index(counts, batch), _stream(stream)))
 
 
@@ -317,7 +327,7 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     dt = torch.float32 if out_f32 else torch.bfloat16
     k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
     v = torch.empty_like(k)
-    _check("wq_kv_read", lib.wq_kv_read(cache.ref, ctypes.byref(_heads(k, dt)), ctypes.byref(_heads(v, dt)), batch, tokens,
+    _check("wq_kv_read", lib.wq_kv_read(cache.ref, _heads(k, dt), _heads(v, dt), batch, tokens,
                                         _index(start, batch), _index(counts, batch), WQ_FLAG_OUT_F32 if out_f32 else 0,
                                         _stream(stream)))
     return k, v
@@ -336,8 +346,7 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
     default dim^-0.5.  max_len: a host-side upper bound of lens if one is known (plans the split of long
     sequences).  out: a [batch, tokens, q_heads, dim] view to write to.  Returns out, or (out, lse) with
     lse fp32 [batch, tokens, q_heads].  Rows that see nothing give 0 and -inf.  workspace: a uint8 tensor of
-    attend_workspace_bytes() bytes; allocated for the call on the current stream when None (pass one with
-    an explicit stream)."""
+    attend_workspace_bytes() bytes that no other call in flight uses; allocated for the call when None."""
     batch, tokens, q_heads, dim = q.shape
     assert dim == cache.dim and batch <= cache.batch
     dt = torch.float32 if out_f32 else torch.bfloat16
@@ -345,10 +354,13 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
         out = torch.empty((batch, tokens, q_heads, dim), dtype=dt, device=q.device)
     assert out.shape == q.shape
     lse = torch.empty((batch, tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
-    need = lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check("wq_attend", lib.wq_attend(cache.ref, ctypes.byref(_heads(q, torch.bfloat16)), ctypes.byref(_heads(out, dt)),
+    if workspace is None:
+        need = lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+    _check("wq_attend", lib.wq_attend(cache.ref, _heads(q, torch.bfloat16), _heads(out, dt),
                                       None if lse is None else lse.data_ptr(), batch, tokens, q_heads,
                                       _index(lens, batch), _index(counts, batch), max_len,
                                       dim ** -0.5 if scale is None else scale, window,
