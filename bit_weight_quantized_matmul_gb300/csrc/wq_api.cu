@@ -154,6 +154,7 @@ int check_cache(const wq_kv_cache* c, KvArgs& a) {
   if (c->page_size == 0 || c->page_size % 16 != 0 || c->page_size > (1 << 30) || c->pages > (int64_t(1) << 31))
     return WQ_ERR_SHAPE;
   if (c->table && c->table_ld > (int64_t(1) << 30)) return WQ_ERR_SHAPE;
+  if ((double)c->pages * c->heads * (double)(c->page_size / 16) >= 2147483648.0) return WQ_ERR_SHAPE;  // 2^35 rows: a terabyte
   if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return WQ_ERR_ARG;
   if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
     return WQ_ERR_ALIGN;

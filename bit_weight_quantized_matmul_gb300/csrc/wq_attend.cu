@@ -29,19 +29,23 @@ namespace wq {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 32;    // tokens per tile
 constexpr int kStages = 3;   // tiles in a warp's ring
 constexpr int kSms = 152;
+// More registers a thread beat more warps: 4, 3 and 2 blocks of NT = 1 an SM read one sequence of 2^20 tokens at
+// 4.6, 5.6 and 5.3 TB/s.
+constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Bytes of one tile of D-element rows: K and V codes, then K and V scales.
-constexpr int stage_bytes(int D) { return 2 * kTile * (D / 2) + 2 * kTile * kv::scale_bytes(D); }
-constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
+// Tokens of a tile: 2 KB of codes for K and for V (32 query rows keep half of it, for their registers).
+constexpr int tile_tokens(int D, int NT) { return NT > 2 ? 32 : 4096 / D; }
+// Bytes of a stage: room for K and V codes, then K and V scales, of a 2 KB tile.
+constexpr int kStageBytes = 2 * 2048 + 2 * 256;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int q_bytes(int D, int NT) { return NT > 2 ? NT * (D / 32) * 32 * 16 : 0; }
 // Joining the warps: O [warp][row][D], then m and l [warp][row].
 constexpr int join_bytes(int D, int NT) { return kWarps * 8 * NT * (D * 4 + 8); }
 constexpr int smem_bytes(int D, int NT) {
-  return (ring_bytes(D) > join_bytes(D, NT) ? ring_bytes(D) : join_bytes(D, NT)) + q_bytes(D, NT);
+  return (kRingBytes > join_bytes(D, NT) ? kRingBytes : join_bytes(D, NT)) + q_bytes(D, NT);
 }
 
 struct Params {
@@ -93,10 +97,10 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 // D = A B + C with C kept.
 __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, float c0, float c1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+                                         uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -122,6 +126,20 @@ __device__ __forceinline__ void signed_pairs(uint32_t w, uint32_t& lo, uint32_t&
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two fp32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ void mul_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
+      "mul.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -160,8 +178,9 @@ __device__ __forceinline__ void ld_shared_cluster_f32x4(uint32_t addr, float (&v
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(const __grid_constant__ Params p) {
   constexpr int NB = D / 32;            // 32-element blocks of a row
+  constexpr int kTile = tile_tokens(D, NT), kGroups = kTile / 16;   // 16 tokens lie in one page
   constexpr int kCodes = kTile * (D / 2), kScales = kTile * kv::scale_bytes(D);
   constexpr bool kQSmem = NT > 2;       // Q fragments live in shared memory instead of registers
   extern __shared__ __align__(128) uint8_t smem[];
@@ -178,6 +197,21 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   const int h = x % a.kv.heads;
   const int64_t b = x / a.kv.heads;
 
+  // Q is asked for first: its addresses need nothing that is still on its way.  Lane (g, q) holds row
+  // 8 j + g's elements 32 blk + 8 q .. + 7 (rows past counts[b] too: they are there, and their columns unused).
+  const int64_t r0 = (int64_t)rt * 8 * NT;                    // first row: token r / group, head r % group
+  uint4 qw[NT][NB];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const uint32_t r = (uint32_t)r0 + 8 * j + g, i = r / (uint32_t)p.group;
+    const bool in = i < a.tokens;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token +
+                          ((int64_t)h * p.group + (r - i * (uint32_t)p.group)) * a.q.head + 8 * q;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+      qw[j][blk] = in ? *reinterpret_cast<const uint4*>(src + 32 * blk) : make_uint4(0, 0, 0, 0);
+  }
+
   // The rows' tokens and what they see.
   const int n = kv::count_of(a.counts, b, a.tokens);
   int len = max(a.lens[b], 0);
@@ -185,7 +219,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     if (threadIdx.x == 0) set_status(WQ_STATUS_ARG);
     len = (int)a.kv.capacity;
   }
-  const int64_t r0 = (int64_t)rt * 8 * NT;                    // first row: token r / group, head r % group
   const int64_t rows = (int64_t)n * p.group;                  // rows of this sequence
   auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)len, (int64_t)len - n + i + 1)) : len; };
   auto lo_of = [&](int64_t i) { return a.window ? (int)max((int64_t)0, (int64_t)len - n + i - a.window + 1) : 0; };
@@ -199,13 +232,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   const int t_end = tile0 + min(ntiles, (split + 1) * per);
   const int t_begin = tile0 + min(ntiles, split * per) + warp;
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * stage_bytes(D);
-  uint8_t* qs = smem + (ring_bytes(D) > join_bytes(D, NT) ? ring_bytes(D) : join_bytes(D, NT));
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
+  uint8_t* qs = smem + (kRingBytes > join_bytes(D, NT) ? kRingBytes : join_bytes(D, NT));
 
   // ---------------------------------------------------------------- streaming tiles
-  // Row number of the tile's half (lane & 1), -1: past the end, -2: no such page.
-  auto locate = [&](int tile) -> int64_t {
-    const int t = tile * kTile + 16 * (lane & 1);
+  // A lane looks up one 16-token group of the warp's next kSpan tiles at a time: row / 16 (a cache of 2^35
+  // rows would not fit the GPU), -1: past the end, -2: no such page.
+  constexpr int kSpan = 32 / kGroups;
+  auto locate = [&](int first) -> int {
+    const int tile = first + lane / kGroups * kWarps, t = tile * kTile + 16 * (lane % kGroups);
     if (tile >= t_end || t >= hi_max) return -1;
     int64_t page = b;
     int off = t;
@@ -218,64 +253,86 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
       set_status(WQ_STATUS_ARG);
       return -2;
     }
-    return (page * a.kv.heads + h) * (int64_t)a.kv.page_size + off;
+    return (int)(page * a.kv.heads + h) * (a.kv.page_size >> 4) + (off >> 4);
   };
-  uint32_t missing = 0;                 // per stage and half: the page is not there
-  auto issue = [&](int tile, int stage, int64_t mine) {
-    const int64_t row[2] = {__shfl_sync(0xFFFFFFFFu, mine, 0), __shfl_sync(0xFFFFFFFFu, mine, 1)};
-    missing = (missing & ~(3u << (2 * stage))) | ((row[0] == -2 ? 1u : 0u) | (row[1] == -2 ? 2u : 0u)) << (2 * stage);
-    const uint32_t dst = ring + stage * stage_bytes(D);
-    // A half's rows are contiguous: lane l copies bytes 16 l .. 16 l + 15 of every 512.
-    const uint32_t to = dst + tile_at<D>(lane / NB, lane % NB);
-    const int64_t own = (lane >> 4) ? row[1] : row[0];
-    const bool whole = row[0] >= 0 && row[1] >= 0 && (tile + 1) * kTile <= hi_max;
-    constexpr int kPer = D / 64;        // 512-byte pieces of a half
+  // Lane l copies bytes 16 l .. 16 l + 15 of every 512 of the codes, and 8 l .. 8 l + 7 of the scales.
+  uint32_t missing = 0;                 // per stage and group: the page is not there
+  const uint32_t to = tile_at<D>(lane / NB, lane % NB);
+  auto issue = [&](int tile, int stage, int mine, int from) {   // from: the lane that holds the first group
+    constexpr int SB = kv::scale_bytes(D), kTokens = 8 / SB;   // tokens whose scales are 8 bytes
+    const uint32_t dst = ring + stage * kStageBytes;
+    int row16[kGroups], least = 0;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t at = row[half] * (D / 2) + lane * 16;
+    for (int u = 0; u < kGroups; ++u) {
+      row16[u] = __shfl_sync(0xFFFFFFFFu, mine, from + u);
+      least = min(least, row16[u]);
+    }
+    constexpr int kPer = D / 64;        // 512-byte pieces of a group
+    if (least >= 0 && (tile + 1) * kTile <= hi_max) {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) {
+        const uint8_t* k = a.kv.codes[0] + lane * 16 + (uint64_t)(uint32_t)row16[u] * (8 * D);
+        const uint8_t* v = a.kv.codes[1] + lane * 16 + (uint64_t)(uint32_t)row16[u] * (8 * D);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          cp16(dst + to + 512 * (u * kPer + j), k + 512 * j, 16);
+          cp16(dst + to + kCodes + 512 * (u * kPer + j), v + 512 * j, 16);
+        }
+      }
+      const int mine16 = __shfl_sync(0xFFFFFFFFu, mine, from + lane * kTokens / 16 % kGroups);
+      if (kScales == 256 || lane < kScales / 8) {
+        const uint64_t at = (uint64_t)(uint32_t)mine16 * (16 * SB) + (lane * kTokens & 15) * SB;
+        cp_small<8>(dst + 2 * kCodes + 8 * lane, a.kv.scales[0] + at, 8);
+        cp_small<8>(dst + 2 * kCodes + kScales + 8 * lane, a.kv.scales[1] + at, 8);
+      }
+      missing &= ~(15u << (4 * stage));
+      return;
+    }
+    uint32_t gone = 0;
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+      const int64_t row = row16[u] < 0 ? -1 : (int64_t)row16[u] * 16;
+      gone |= (row16[u] == -2 ? 1u : 0u) << u;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int r = 16 * half + (512 * j + 16 * lane) / (D / 2);
-        const bool in = whole || (row[half] >= 0 && tile * kTile + r < hi_max);
-        cp16(to + (half * kPer + j) * 512, a.kv.codes[0] + (in ? at + 512 * j : 0), in ? 16 : 0);
-        cp16(to + kCodes + (half * kPer + j) * 512, a.kv.codes[1] + (in ? at + 512 * j : 0), in ? 16 : 0);
+        const int r = (512 * j + 16 * lane) / (D / 2);
+        const bool in = row >= 0 && tile * kTile + 16 * u + r < hi_max;
+        const int64_t at = in ? row * (D / 2) + 512 * j + 16 * lane : 0;
+        cp16(dst + to + (u * kPer + j) * 512, a.kv.codes[0] + at, in ? 16 : 0);
+        cp16(dst + to + kCodes + (u * kPer + j) * 512, a.kv.codes[1] + at, in ? 16 : 0);
+      }
+      if (lane * kTokens / 16 == u) {
+        const int left = hi_max - (tile * kTile + lane * kTokens);   // tokens from this lane's first one on
+        const int bytes = row >= 0 ? min(max(left, 0), kTokens) * SB : 0;
+        const int64_t at = bytes ? (row + (lane * kTokens & 15)) * SB : 0;
+        cp_small<8>(dst + 2 * kCodes + 8 * lane, a.kv.scales[0] + at, bytes);
+        cp_small<8>(dst + 2 * kCodes + kScales + 8 * lane, a.kv.scales[1] + at, bytes);
       }
     }
-    const bool in = whole || (own >= 0 && tile * kTile + lane < hi_max);
-    const int64_t at = in ? (own + (lane & 15)) * kv::scale_bytes(D) : 0;
-    cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + lane * kv::scale_bytes(D), a.kv.scales[0] + at,
-                                 in ? kv::scale_bytes(D) : 0);
-    cp_small<kv::scale_bytes(D)>(dst + 2 * kCodes + kScales + lane * kv::scale_bytes(D), a.kv.scales[1] + at,
-                                 in ? kv::scale_bytes(D) : 0);
+    missing = (missing & ~(15u << (4 * stage))) | gone << (4 * stage);
   };
-  int64_t next = locate(t_begin);
+  int rows_now = locate(t_begin), rows_next = locate(t_begin + kSpan * kWarps);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (t_begin + s * kWarps < t_end) issue(t_begin + s * kWarps, s, next);
+    if (t_begin + s * kWarps < t_end) issue(t_begin + s * kWarps, s, rows_now, s * kGroups);
     cp_commit();
-    next = locate(t_begin + (s + 1) * kWarps);
   }
 
   // ---------------------------------------------------------------- Q
-  // Lane (g, q) holds row 8 j + g's elements 32 blk + 8 q .. + 7.  The row is multiplied by 2^e, which
-  // brings its largest element to 2^12 .. 2^13.
+  // A row is multiplied by 2^e, which brings its largest element to 2^12 .. 2^13.
   uint32_t qf[kQSmem ? 1 : NT][NB][4];
-  float init[NT][FMT == WQ_Q4_0 ? NB : 1][2];   // q4_0: -8 sum(Q) of a block, columns 2q and 2q + 1
+  // q4_0: -8 sum(Q) of a block, columns 2q and 2q + 1, twice: an accumulator's four registers, kept as such
+  // (two of them would be copied for every MMA)
+  float init[NT][FMT == WQ_Q4_0 ? NB : 1][4];
   float fac[NT][2];                             // accumulated score -> score in base 2
   const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t r = r0 + 8 * j + g;
     uint32_t u[NB][4];
-    const bool in = r < rows;
-    const int64_t i = in ? r / p.group : 0;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token +
-                          ((int64_t)h * p.group + (in ? r - i * p.group : 0)) * a.q.head + 8 * q;
     float amax = 0.0f;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-      const uint4 w = in ? *reinterpret_cast<const uint4*>(src + 32 * blk) : make_uint4(0, 0, 0, 0);
-      u[blk][0] = w.x; u[blk][1] = w.y; u[blk][2] = w.z; u[blk][3] = w.w;
+      u[blk][0] = qw[j][blk].x; u[blk][1] = qw[j][blk].y; u[blk][2] = qw[j][blk].z; u[blk][3] = qw[j][blk].w;
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(bf16_bits_to_f32((u[blk][e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
     }
@@ -310,6 +367,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
         sum *= -8.0f * 5.9604644775390625e-8f;   // -8 * 2^-24
         init[j][FMT == WQ_Q4_0 ? blk : 0][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * q);
         init[j][FMT == WQ_Q4_0 ? blk : 0][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * q + 4);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          asm volatile("mov.f32 %0, %1;" : "=f"(init[j][FMT == WQ_Q4_0 ? blk : 0][2 + c]) : "f"(init[j][FMT == WQ_Q4_0 ? blk : 0][c]));
       }
     }
     const float f = a.scale * kLog2e * (FMT == WQ_Q4_0 ? 16777216.0f : kg) * down;
@@ -341,154 +401,162 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   }
 
   // ---------------------------------------------------------------- tiles
-  // One tile; MASKED: some row does not see all of it.
+  // This lane's row address for ldmatrix: four blocks of eight tokens (D = 128), or two of sixteen.
+  const uint32_t lane_at = D == 128 ? tile_at<D>(lane & 7, lane >> 3) : tile_at<D>(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
+  // One tile; masked: some row does not see all of it.
   auto work = [&](auto masked_c, int tile, int stage, uint32_t gone) {
     constexpr bool masked = decltype(masked_c)::value;
-    const uint32_t base = ring + stage * stage_bytes(D);
+    const uint32_t base = ring + stage * kStageBytes;
     const uint8_t* gen = smem + (base - smem_u32(smem));
-    // ---- scores of 2 x 16 tokens
-    float s[2][NT][4];
+    // ---- scores, two groups at a time
+    float s[kGroups][NT][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kGroups; ++u)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[u][j][k] = 0.0f;
-    uint32_t kw[2][2][4];               // [group][token g or g + 8][block]
-    float kd[2][2][FMT == WQ_Q4_0 ? NB : 1];
-    uint32_t ks[2][2][FMT == WQ_NVFP4 ? NB : 1];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (NB == 4) {
+    for (int u0 = 0; u0 < kGroups; u0 += 2) {
+      uint32_t kw[2][2][4];               // [group][token g or g + 8][block]
+      float kd[2][2][FMT == WQ_Q4_0 ? NB : 1];
+      uint32_t ks[2][2][FMT == WQ_NVFP4 ? NB : 1];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) ldsm(kw[u][hf], base + tile_at<D>(16 * u + 8 * hf + (lane & 7), lane >> 3));
-      } else {
-        uint32_t r[4];
-        ldsm(r, base + tile_at<D>(16 * u + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
-        kw[u][0][0] = r[0]; kw[u][0][1] = r[1]; kw[u][1][0] = r[2]; kw[u][1][1] = r[3];
-      }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint8_t* sp = gen + 2 * kCodes + (16 * u + 8 * hf + g) * kv::scale_bytes(D);
-        uint32_t w[2];
+      for (int u = 0; u < 2; ++u) {
         if (NB == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(sp);
-          w[0] = v.x; w[1] = v.y;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) ldsm(kw[u][hf], base + lane_at + (16 * (u0 + u) + 8 * hf) * (D / 2));
         } else {
-          w[0] = w[1] = *reinterpret_cast<const uint32_t*>(sp);
+          uint32_t r[4];
+          ldsm(r, base + lane_at + 16 * (u0 + u) * (D / 2));
+          kw[u][0][0] = r[0]; kw[u][0][1] = r[1]; kw[u][1][0] = r[2]; kw[u][1][1] = r[3];
         }
-        if (FMT == WQ_Q4_0) {
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk)
-            kd[u][hf][FMT == WQ_Q4_0 ? blk : 0] = f16_bits_to_f32((w[blk >> 1] >> (16 * (blk & 1))) & 0xFFFFu);
-        } else {
-          // the word of lane q lies in the 16-block q >> 1 of its 32 elements
-          const uint32_t sel = (q >> 1) ? 0x3311u : 0x2200u;
-#pragma unroll
-          for (int pr = 0; pr < NB / 2; ++pr)
-            e4m3_pairs(__byte_perm(w[pr], 0, sel), ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr : 0], ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr + 1 : 0]);
-        }
-      }
-    }
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      uint32_t av[2][2][4];             // [group][token g or g + 8][pair]
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t w = kw[u][hf][blk];
-          if (FMT == WQ_Q4_0) {
-            av[u][hf][0] = w & 0x000F000Fu;
-            av[u][hf][1] = w & 0x00F000F0u;
-            av[u][hf][2] = (w >> 8) & 0x000F000Fu;
-            av[u][hf][3] = (w >> 8) & 0x00F000F0u;
+          const uint8_t* sp = gen + 2 * kCodes + (16 * (u0 + u) + 8 * hf + g) * kv::scale_bytes(D);
+          uint32_t w[2];
+          if (NB == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sp);
+            w[0] = v.x; w[1] = v.y;
           } else {
-            kv::e2m1_pairs(w, av[u][hf]);
+            w[0] = w[1] = *reinterpret_cast<const uint32_t*>(sp);
+          }
+          if (FMT == WQ_Q4_0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) av[u][hf][e] = mul2(av[u][hf][e], ks[u][hf][FMT == WQ_NVFP4 ? blk : 0]);
+            for (int blk = 0; blk < NB; ++blk)
+              kd[u][hf][FMT == WQ_Q4_0 ? blk : 0] = f16_bits_to_f32((w[blk >> 1] >> (16 * (blk & 1))) & 0xFFFFu);
+          } else {
+            // the word of lane q lies in the 16-block q >> 1 of its 32 elements
+            const uint32_t sel = (q >> 1) ? 0x3311u : 0x2200u;
+#pragma unroll
+            for (int pr = 0; pr < NB / 2; ++pr)
+              e4m3_pairs(__byte_perm(w[pr], 0, sel), ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr : 0], ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr + 1 : 0]);
           }
         }
+      }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint32_t f[4];
-        if (kQSmem) {
-          const uint4 v = reinterpret_cast<const uint4*>(qs)[(j * NB + blk) * 32 + lane];
-          f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-        } else {
+      for (int blk = 0; blk < NB; ++blk) {
+        uint32_t av[2][2][4];             // [group][token g or g + 8][pair]
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = qf[kQSmem ? 0 : j][blk][e];
-        }
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (FMT == WQ_Q4_0) {
-            const int ib = FMT == WQ_Q4_0 ? blk : 0;
-            float c[4];
-            mma_from(c, av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1], init[j][ib][0], init[j][ib][1]);
-            mma(c, av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t w = kw[u][hf][blk];
+            if (FMT == WQ_Q4_0) {
+              av[u][hf][0] = w & 0x000F000Fu;
+              av[u][hf][1] = w & 0x00F000F0u;
+              av[u][hf][2] = (w >> 8) & 0x000F000Fu;
+              av[u][hf][3] = (w >> 8) & 0x00F000F0u;
+            } else {
+              kv::e2m1_pairs(w, av[u][hf]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[u][j][k] = fmaf(kd[u][k >> 1][ib], c[k], s[u][j][k]);
+              for (int e = 0; e < 4; ++e) av[u][hf][e] = mul2(av[u][hf][e], ks[u][hf][FMT == WQ_NVFP4 ? blk : 0]);
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t f[4];
+          if (kQSmem) {
+            const uint4 v = reinterpret_cast<const uint4*>(qs)[(j * NB + blk) * 32 + lane];
+            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
           } else {
-            mma(s[u][j], av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1]);
-            mma(s[u][j], av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = qf[kQSmem ? 0 : j][blk][e];
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (FMT == WQ_Q4_0) {
+              const int ib = FMT == WQ_Q4_0 ? blk : 0;
+              float c[4];
+              mma_from(c, av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1], init[j][ib]);
+              mma(c, av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[u0 + u][j][k] = fmaf(kd[u][k >> 1][ib], c[k], s[u0 + u][j][k]);
+            } else {
+              mma(s[u0 + u][j], av[u][0][0], av[u][1][0], av[u][0][1], av[u][1][1], f[0], f[1]);
+              mma(s[u0 + u][j], av[u][0][2], av[u][1][2], av[u][0][3], av[u][1][3], f[2], f[3]);
+            }
           }
         }
       }
     }
 
     // ---- online softmax: c[0], c[1] are token g's columns 2q, 2q + 1, c[2], c[3] token g + 8's
-    bool moved = false;
-    uint32_t pf[2][NT][2];              // p as fp16 pairs of columns: tokens g, g + 8
+    uint32_t pf[kGroups][NT][2];              // p as fp16 pairs of columns: tokens g, g + 8
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kGroups; ++u) {
+        float (&v)[4] = s[u][j];
+        mul_pair(v[0], v[1], fac[j][0], fac[j][1]);
+        mul_pair(v[2], v[3], fac[j][0], fac[j][1]);
+        if (masked) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& v = s[u][j][k];
-          v *= fac[j][k & 1];
-          if (masked) {
+          for (int k = 0; k < 4; ++k) {
             const int t = tile * kTile + 16 * u + 8 * (k >> 1) + g;
-            if (t < c_lo[j][k & 1] || t >= c_hi[j][k & 1] || ((gone >> u) & 1u)) v = -INFINITY;
+            if (t < c_lo[j][k & 1] || t >= c_hi[j][k & 1] || ((gone >> u) & 1u)) v[k] = -INFINITY;
           }
-          top[k & 1] = fmaxf(top[k & 1], v);
         }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], d));
-        moved = moved || top[c] > m[j][c];
-        top[c] = fmaxf(top[c], m[j][c]);
+        top[0] = max3(top[0], v[0], v[2]);
+        top[1] = max3(top[1], v[1], v[3]);
       }
-      const float base0 = top[0] == -INFINITY ? 0.0f : top[0], base1 = top[1] == -INFINITY ? 0.0f : top[1];
-      const float f0 = ex2(m[j][0] - base0), f1 = ex2(m[j][1] - base1);
-      m[j][0] = top[0];
-      m[j][1] = top[1];
-      float add[2] = {0.0f, 0.0f};
+      // most tiles of a long sequence move no maximum: then nothing is exchanged or rescaled
+      if (__any_sync(0xFFFFFFFFu, top[0] > m[j][0] || top[1] > m[j][1])) {
+        float f[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s[u][j][k] = ex2(s[u][j][k] - ((k & 1) ? base1 : base0));
-          add[k & 1] += s[u][j][k];
+          for (int d = 4; d < 32; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], d));
+          top[c] = fmaxf(top[c], m[j][c]);
+          f[c] = ex2(m[j][c] + (top[c] == -INFINITY ? 0.0f : -top[c]));
+          m[j][c] = top[c];
+          l[j][c] *= f[c];
         }
-        pf[u][j][0] = pack_f16x2(s[u][j][0], s[u][j][1]);
-        pf[u][j][1] = pack_f16x2(s[u][j][2], s[u][j][3]);
-      }
-      l[j][0] = fmaf(l[j][0], f0, add[0]);
-      l[j][1] = fmaf(l[j][1], f1, add[1]);
-      if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
         for (int d = 0; d < 2 * NB; ++d) {
-          o[j][d][0] *= f0; o[j][d][1] *= f1; o[j][d][2] *= f0; o[j][d][3] *= f1;
+          mul_pair(o[j][d][0], o[j][d][1], f[0], f[1]);
+          mul_pair(o[j][d][2], o[j][d][3], f[0], f[1]);
         }
+      }
+      const float base0 = m[j][0] == -INFINITY ? 0.0f : -m[j][0], base1 = m[j][1] == -INFINITY ? 0.0f : -m[j][1];
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) {
+        float (&v)[4] = s[u][j];
+        add_pair(v[0], v[1], base0, base1);
+        add_pair(v[2], v[3], base0, base1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = ex2(v[k]);
+        add_pair(l[j][0], l[j][1], v[0], v[1]);
+        add_pair(l[j][0], l[j][1], v[2], v[3]);
+        pf[u][j][0] = pack_f16x2(v[0], v[1]);
+        pf[u][j][1] = pack_f16x2(v[2], v[3]);
       }
     }
 
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kGroups; ++u) {
       uint32_t pb[NT][2];               // B operand: row g's tokens 2q, 2q + 1 and 2q + 8, 2q + 9
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -498,10 +566,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
       uint32_t vw[2][4];                // [tokens 0 .. 7 or 8 .. 15][block]
       if (NB == 4) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) ldsm_t(vw[hf], base + kCodes + tile_at<D>(16 * u + 8 * hf + (lane & 7), lane >> 3));
+        for (int hf = 0; hf < 2; ++hf) ldsm_t(vw[hf], base + kCodes + lane_at + (16 * u + 8 * hf) * (D / 2));
       } else {
         uint32_t r[4];
-        ldsm_t(r, base + kCodes + tile_at<D>(16 * u + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+        ldsm_t(r, base + kCodes + lane_at + 16 * u * (D / 2));
         vw[0][0] = r[0]; vw[0][1] = r[1]; vw[1][0] = r[2]; vw[1][1] = r[3];
       }
       uint32_t vs[2][4];                // scales of tokens (2q, 2q + 1) + 8 hf as fp16 pairs, per 32-block
@@ -538,14 +606,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
             signed_pairs(w, av[hf][0], av[hf][1]);
             signed_pairs(w >> 8, av[hf][2], av[hf][3]);
           } else {
-            // bytes (token 2q in the low nibble, 2q + 1 in the high): elements 0, 2, 1, 3
-            const uint32_t ev = (w & 0x0F0Fu) | ((w >> 12) & 0xF0F0u), od = ((w >> 4) & 0x0F0Fu) | ((w >> 16) & 0xF0F0u);
+            // pairs of elements 0, 1 and 2, 3 of token 2q, then of token 2q + 1
             uint32_t r[4];
-            kv::e2m1_pairs(__byte_perm(ev, od, 0x5410u), r);
-            av[hf][0] = mul2(r[0], vs[hf][blk]);
-            av[hf][2] = mul2(r[1], vs[hf][blk]);
-            av[hf][1] = mul2(r[2], vs[hf][blk]);
-            av[hf][3] = mul2(r[3], vs[hf][blk]);
+            kv::e2m1_pairs(w, r);
+            av[hf][0] = mul2(__byte_perm(r[0], r[2], 0x5410u), vs[hf][blk]);
+            av[hf][1] = mul2(__byte_perm(r[0], r[2], 0x7632u), vs[hf][blk]);
+            av[hf][2] = mul2(__byte_perm(r[1], r[3], 0x5410u), vs[hf][blk]);
+            av[hf][3] = mul2(__byte_perm(r[1], r[3], 0x7632u), vs[hf][blk]);
           }
         }
 #pragma unroll
@@ -565,19 +632,24 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
       }
     }
   };
-  int stage = 0;
+  int stage = 0, from = (kStages - 1) * kGroups;
   for (int tile = t_begin; tile < t_end; tile += kWarps) {
     {
       const int ahead = tile + (kStages - 1) * kWarps;
       int s = stage + kStages - 1;
       if (s >= kStages) s -= kStages;
-      if (ahead < t_end) issue(ahead, s, next);
+      if (from == 32) {                 // the next kSpan tiles' rows; those after them come in meanwhile
+        from = 0;
+        rows_now = rows_next;
+        rows_next = locate(ahead + kSpan * kWarps);
+      }
+      if (ahead < t_end) issue(ahead, s, rows_now, from);
+      from += kGroups;
       cp_commit();
-      next = locate(ahead + kWarps);
     }
     cp_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t gone = (missing >> (2 * stage)) & 3u;
+    const uint32_t gone = (missing >> (4 * stage)) & 15u;
     if (gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min) work(std::true_type{}, tile, stage, gone);
     else work(std::false_type{}, tile, stage, 0u);
     if (++stage == kStages) stage = 0;
@@ -618,8 +690,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
       }
   __syncthreads();
   // Thread t of a row's kPerRow takes its elements 4 t, 4 t + 4 kPerRow, ...
-  constexpr int kRows = 8 * NT, kPerRow = 32 * kWarps / kRows;
-  const int row = threadIdx.x / kPerRow, part = threadIdx.x % kPerRow;
+  constexpr int kRows = 8 * NT, kPerRow = 32 * kWarps / kRows < D / 4 ? 32 * kWarps / kRows : D / 4;
+  const bool joins = threadIdx.x < kRows * kPerRow;
+  const int row = joins ? threadIdx.x / kPerRow : 0, part = joins ? threadIdx.x % kPerRow : 0;
   float top = -INFINITY, sum = 0.0f, f[kWarps];
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * kRows + row].x);
@@ -652,8 +725,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     step = p.cluster;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < D / (4 * kPerRow); ++k) *reinterpret_cast<float4*>(so + row * D + 4 * (part + k * kPerRow)) = acc[k];
-    if (part == 0) sml[row] = make_float2(top, sum);
+    for (int k = 0; k < D / (4 * kPerRow); ++k)
+      if (joins) *reinterpret_cast<float4*>(so + row * D + 4 * (part + k * kPerRow)) = acc[k];
+    if (joins && part == 0) sml[row] = make_float2(top, sum);
     cluster_sync();
     float2 ml[8];
 #pragma unroll
@@ -693,7 +767,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
   }
 
   const int64_t r = r0 + row, i = r / p.group;
-  if (p.parts > 1) {
+  if (!joins) {
+  } else if (p.parts > 1) {
     const int64_t slot = (tile_id * p.parts + split / p.cluster) * kRows + row;
     if (part == 0 && first == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
 #pragma unroll
@@ -717,13 +792,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attend_kernel(co
     if (a.lse && part == 0 && first == 0)
       a.lse[(b * a.tokens + i) * a.q_heads + hq] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
   }
+  griddep_launch_dependents();
   if (p.cluster > 1) cluster_sync();    // the others may still read this block's shared memory
 }
 
 // Joins the parts of a query row and head: a block per row, its warps over the parts, lanes over
-// the elements, then the warps in order.
+// the elements, then the warps in order.  Launched while the attention kernel runs; it waits for it.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tile_rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p, int tile_rows) {
   const AttendArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t id = blockIdx.x;        // (sequence, token, head)
@@ -732,7 +809,8 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   const int64_t r = i * p.group + (hq - h * p.group);
   const int parts = i < kv::count_of(a.counts, b, a.tokens) ? p.parts : 0;
   const int64_t slot = ((b * a.kv.heads + h) * p.row_tiles + r / tile_rows) * p.parts * tile_rows + r % tile_rows;
-  __shared__ float so[4][D], sl[4];
+  __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
+  griddep_wait();
   float top = -INFINITY, sum = 0.0f, o[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
@@ -740,7 +818,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll 4
-  for (int s = warp; s < parts; s += 4) {
+  for (int s = warp; s < parts; s += kJoinWarps) {
     const int64_t at = slot + (int64_t)s * tile_rows;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
     const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
@@ -753,9 +831,14 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   if (lane == 0) sl[warp] = sum;
   __syncthreads();
   if (threadIdx.x >= D) return;
-  sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  sum = 0.0f;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    sum += sl[w];
+    v += so[w][threadIdx.x];
+  }
   const bool some = sum != 0.0f;
-  const float v = (so[0][threadIdx.x] + so[1][threadIdx.x]) + (so[2][threadIdx.x] + so[3][threadIdx.x]);
   const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head + threadIdx.x;
   put(a, at, some ? v * (1.0f / sum) : 0.0f);
   if (a.lse && threadIdx.x == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
@@ -774,11 +857,12 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   const int64_t blocks = batch * kv.heads * pl.row_tiles;
   int64_t seen = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
   if (window > 0 && window + tokens < seen) seen = window + tokens;
-  const int64_t tiles = (seen + kTile - 1) / kTile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
-  int64_t want = (int64_t)kSms * (pl.nt == 1 ? 4 : 2) / (blocks > 0 ? blocks : 1);
+  const int tile = tile_tokens(kv.dim, pl.nt);
+  const int64_t tiles = (seen + tile - 1) / tile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
+  int64_t want = (int64_t)kSms * blocks_per_sm(pl.nt) / (blocks > 0 ? blocks : 1);
   if (want > most) want = most;
-  pl.cluster = want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
-  pl.parts = (int)(want / pl.cluster < 1 ? 1 : want / pl.cluster);
+  pl.cluster = want > 8 ? 1 : want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
+  pl.parts = want > 8 ? (int)want : 1;
   pl.slots = pl.parts > 1 ? (size_t)(blocks * pl.parts * 8 * pl.nt) : 0;
   return pl;
 }
@@ -804,7 +888,17 @@ int launch(const Params& p, cudaStream_t s) {
   if (cudaLaunchKernelEx(&cfg, attend_kernel<FMT, D, NT>, p) != cudaSuccess) return WQ_ERR_CUDA;
   count_launch();
   if (p.parts > 1) {
-    join_kernel<D><<<(unsigned)(p.a.batch * p.a.tokens * p.a.q_heads), 128, 0, s>>>(p, 8 * NT);
+    const int64_t blocks = p.a.batch * p.a.tokens * p.a.q_heads;
+    if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+    cudaLaunchConfig_t jc{};
+    jc.gridDim = dim3((unsigned)blocks);
+    jc.blockDim = dim3(32 * kJoinWarps);
+    jc.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    jc.attrs = at;
+    jc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&jc, join_kernel<D>, p, 8 * NT) != cudaSuccess) return WQ_ERR_CUDA;
     count_launch();
   }
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;

@@ -30,8 +30,9 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
 }
 
 // Row (of the [pages, heads, page_size] rows) of position t of sequence b and head h, or -1 (and
-// WQ_ERR_ARG in the status word) where the position or its table entry lies outside the cache.
-__device__ __forceinline__ int64_t row_of(const KvArgs& kv, int64_t b, int64_t t, int h) {
+// WQ_ERR_ARG in the status word) where the position or its table entry lies outside the cache.  *left: the
+// tokens from t to the end of its page, whose rows follow.
+__device__ __forceinline__ int64_t row_of(const KvArgs& kv, int64_t b, int64_t t, int h, int* left) {
   int64_t page = b;
   int off = (int)t;
   bool ok = t >= 0 && t < kv.capacity;
@@ -45,6 +46,7 @@ __device__ __forceinline__ int64_t row_of(const KvArgs& kv, int64_t b, int64_t t
     set_status(WQ_STATUS_ARG);
     return -1;
   }
+  *left = kv.page_size - off;
   return (page * kv.heads + h) * (int64_t)kv.page_size + off;
 }
 
