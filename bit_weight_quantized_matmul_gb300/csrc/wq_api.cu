@@ -471,8 +471,9 @@ int wq_selftest_encoders(const float* in, int64_t n, uint8_t* out, void* stream)
 int wq_last_device_status(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
   int worst = WQ_OK;
-  const int parts[8] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
-                        take_status_w4a4(), take_status_w4a16(), take_status_kv(), take_status_attend()};
+  const int parts[9] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
+                        take_status_w4a4(), take_status_w4a16(), take_status_kv(), take_status_attend(),
+                        take_status_attend_tc()};
   for (int v : parts)
     if (v != WQ_OK) worst = v;
   return worst;

@@ -31,6 +31,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;   // tiles in a warp's ring
 constexpr int kSms = 152;
+#ifndef TCROWS
+#define TCROWS 32
+#endif
 // More registers a thread beat more warps: 4, 3 and 2 blocks of NT = 1 an SM read one sequence of 2^20 tokens at
 // 4.6, 5.6 and 5.3 TB/s.
 constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -147,15 +150,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Four E4M3 bytes -> two fp16 pairs.
-__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 h0, h1;\n\t"
-      "mov.b32 {h0, h1}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, h0;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, h1;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(w));
-}
-
 // Which of a lane's eight elements of a block pair p of a K operand holds (see the K unpacking).
 template <int FMT>
 __device__ __forceinline__ constexpr int pair_lo(int p) { return FMT == WQ_Q4_0 ? p : 2 * p; }
@@ -182,6 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   constexpr int NB = D / 32;            // 32-element blocks of a row
   constexpr int kTile = tile_tokens(D, NT), kGroups = kTile / 16;   // 16 tokens lie in one page
   constexpr int kCodes = kTile * (D / 2), kScales = kTile * kv::scale_bytes(D);
+  // p = 2^(score - m + kUp): NVFP4's weights use fp16's upper range too (q4_0's are still to be multiplied by d)
+  constexpr float kUp = FMT == WQ_NVFP4 ? 15.0f : 0.0f;
   constexpr bool kQSmem = NT > 2;       // Q fragments live in shared memory instead of registers
   extern __shared__ __align__(128) uint8_t smem[];
   const AttendArgs& a = p.a;
@@ -450,7 +446,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
             const uint32_t sel = (q >> 1) ? 0x3311u : 0x2200u;
 #pragma unroll
             for (int pr = 0; pr < NB / 2; ++pr)
-              e4m3_pairs(__byte_perm(w[pr], 0, sel), ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr : 0], ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr + 1 : 0]);
+              kv::e4m3_pairs(__byte_perm(w[pr], 0, sel), ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr : 0], ks[u][hf][FMT == WQ_NVFP4 ? 2 * pr + 1 : 0]);
           }
         }
       }
@@ -539,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
           mul_pair(o[j][d][2], o[j][d][3], f[0], f[1]);
         }
       }
-      const float base0 = m[j][0] == -INFINITY ? 0.0f : -m[j][0], base1 = m[j][1] == -INFINITY ? 0.0f : -m[j][1];
+      const float base0 = m[j][0] == -INFINITY ? 0.0f : kUp - m[j][0], base1 = m[j][1] == -INFINITY ? 0.0f : kUp - m[j][1];
 #pragma unroll
       for (int u = 0; u < kGroups; ++u) {
         float (&v)[4] = s[u][j];
@@ -592,7 +588,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
             vs[hf][2 * pr + 1] = __byte_perm(t0[pr], t1[pr], 0x7632u);
           } else {
             // four codes of lane g lie in the 16-block g >> 2 of the 32 elements
-            e4m3_pairs(__byte_perm(t0[pr], t1[pr], (g >> 2) ? 0x7351u : 0x6240u), vs[hf][2 * pr], vs[hf][2 * pr + 1]);
+            kv::e4m3_pairs(__byte_perm(t0[pr], t1[pr], (g >> 2) ? 0x7351u : 0x6240u), vs[hf][2 * pr], vs[hf][2 * pr + 1]);
           }
         }
       }
@@ -673,7 +669,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) sml[warp * 8 * NT + 8 * j + 2 * q + c] = make_float2(m[j][c], l[j][c]);
+      for (int c = 0; c < 2; ++c) sml[warp * 8 * NT + 8 * j + 2 * q + c] = make_float2(m[j][c] - kUp, l[j][c]);
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -845,18 +841,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 }
 
 struct Plan {
+  bool tc;           // the tensor-memory kernel
   int nt, row_tiles, cluster, parts;
+  AttendTcPlan tcp;
   size_t slots;      // partial rows in the workspace
 };
 
 Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, int64_t window) {
   Plan pl{};
   const int64_t group = q_heads / kv.heads, rows = tokens * group;
+  // The window only ever lowers the number of parts, so that the workspace without it suffices.
+  const int64_t held = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
+  const int64_t seen = window > 0 && window + tokens < held ? window + tokens : held;
+  pl.tc = rows > TCROWS;
+  if (pl.tc) {
+    // two groups of rows a block where that leaves a block for every SM; tokens are shared where it does not,
+    // four tiles of 128 to a part at least
+    const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
+    pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
+    if (half == 1) pl.tcp.groups = 1;
+    pl.tcp.row_tiles = (int)((half + pl.tcp.groups - 1) / pl.tcp.groups);
+    const int64_t tiles = (seen + 127) / 128, most = (tiles + 3) / 4, room = kSms * (kv.dim == 64 && pl.tcp.groups == 1 ? 2 : 1);
+    int64_t want = room / (heads * pl.tcp.row_tiles);
+    if (want > most) want = most;
+    pl.tcp.parts = (int)(want > 1 ? want : 1);
+    pl.tcp.slots = pl.tcp.parts > 1 ? (size_t)(heads * pl.tcp.row_tiles * pl.tcp.parts * pl.tcp.groups * 128) : 0;
+    pl.parts = pl.tcp.parts;
+    pl.slots = pl.tcp.slots;
+    return pl;
+  }
   pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   pl.row_tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
   const int64_t blocks = batch * kv.heads * pl.row_tiles;
-  int64_t seen = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
-  if (window > 0 && window + tokens < seen) seen = window + tokens;
   const int tile = tile_tokens(kv.dim, pl.nt);
   const int64_t tiles = (seen + tile - 1) / tile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
   int64_t want = (int64_t)kSms * blocks_per_sm(pl.nt) / (blocks > 0 ? blocks : 1);
@@ -865,6 +881,24 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   pl.parts = want > 8 ? (int)want : 1;
   pl.slots = pl.parts > 1 ? (size_t)(blocks * pl.parts * 8 * pl.nt) : 0;
   return pl;
+}
+
+template <int D>
+int launch_join(const Params& p, int tile_rows, cudaStream_t s) {
+  const int64_t blocks = p.a.batch * p.a.tokens * p.a.q_heads;
+  if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  cudaLaunchConfig_t jc{};
+  jc.gridDim = dim3((unsigned)blocks);
+  jc.blockDim = dim3(32 * kJoinWarps);
+  jc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  jc.attrs = at;
+  jc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&jc, join_kernel<D>, p, tile_rows) != cudaSuccess) return WQ_ERR_CUDA;
+  count_launch();
+  return WQ_OK;
 }
 
 template <int FMT, int D, int NT>
@@ -888,18 +922,8 @@ int launch(const Params& p, cudaStream_t s) {
   if (cudaLaunchKernelEx(&cfg, attend_kernel<FMT, D, NT>, p) != cudaSuccess) return WQ_ERR_CUDA;
   count_launch();
   if (p.parts > 1) {
-    const int64_t blocks = p.a.batch * p.a.tokens * p.a.q_heads;
-    if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
-    cudaLaunchConfig_t jc{};
-    jc.gridDim = dim3((unsigned)blocks);
-    jc.blockDim = dim3(32 * kJoinWarps);
-    jc.stream = s;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    jc.attrs = at;
-    jc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&jc, join_kernel<D>, p, 8 * NT) != cudaSuccess) return WQ_ERR_CUDA;
-    count_launch();
+    const int rc = launch_join<D>(p, 8 * NT, s);
+    if (rc != WQ_OK) return rc;
   }
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
@@ -919,11 +943,16 @@ int attend(const AttendArgs& a, cudaStream_t s) {
   Params p{};
   p.a = a;
   p.group = (int)(a.q_heads / a.kv.heads);
-  p.row_tiles = pl.row_tiles;
+  p.row_tiles = pl.tc ? pl.tcp.row_tiles : pl.row_tiles;
   p.cluster = pl.cluster;
   p.parts = pl.parts;
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = p.part_o + pl.slots * a.kv.dim;
+  if (pl.tc) {
+    const int rc = attend_tc(a, pl.tcp, s);
+    if (rc != WQ_OK || pl.parts == 1) return rc;
+    return a.kv.dim == 64 ? launch_join<64>(p, 128 * pl.tcp.groups, s) : launch_join<128>(p, 128 * pl.tcp.groups, s);
+  }
   if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? launch_nt<WQ_Q4_0, 64>(p, pl.nt, s) : launch_nt<WQ_Q4_0, 128>(p, pl.nt, s);
   return a.kv.dim == 64 ? launch_nt<WQ_NVFP4, 64>(p, pl.nt, s) : launch_nt<WQ_NVFP4, 128>(p, pl.nt, s);
 }

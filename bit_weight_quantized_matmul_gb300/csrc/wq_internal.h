@@ -152,6 +152,14 @@ struct AttendArgs {
 size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len);
 int attend(const AttendArgs& a, cudaStream_t s);
 int take_status_attend();
+// Many query rows per cached head (wq_attend_tc.cu): groups of 128 rows a block, blocks that share the
+// tokens of a row tile (parts > 1: partial rows to the workspace, joined afterwards).
+struct AttendTcPlan {
+  int groups, row_tiles, parts;
+  size_t slots;
+};
+int attend_tc(const AttendArgs& a, const AttendTcPlan& pl, cudaStream_t s);
+int take_status_attend_tc();
 
 // driver entry point for tensor-map encoding (resolved once through the runtime)
 bool encode_tmap_2d(void* tmap, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,

@@ -29,6 +29,15 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
 }
 
+// Four E4M3 bytes -> two fp16 pairs, exact.
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "mov.b32 {h0, h1}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, h0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h1;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
 // Row (of the [pages, heads, page_size] rows) of position t of sequence b and head h, or -1 (and
 // WQ_ERR_ARG in the status word) where the position or its table entry lies outside the cache.  *left: the
 // tokens from t to the end of its page, whose rows follow.
