@@ -22,6 +22,12 @@
 // A V scale that is no finite number cannot be left to the product (0 * NaN spoils rows that do not see
 // the token): the block is stored as zeros and the rows that do see the token are made NaN.
 //
+// Measured on GB300 (2 x 8 heads of 128 x 128 tokens of a group of 2, 19 sequences of 16384, one block an SM): 1075 TFLOP/s
+// (q4_0), 1130 (NVFP4), 0.56 and 0.59 of the measured bf16 rate; a tile of 128 tokens takes 4500 cycles, of which
+// a row's softmax 2300 and the tensor cores' work for its group 1100 follow one another.  Tried and slower: half
+// tiles of 64 tokens with scores ahead of the products (more, smaller MMAs: 815 TFLOP/s); one pass over S with
+// P kept in registers (915); a row's 128 scores in registers (spills).
+//
 // Every wait is bounded; after one ran out the roles stop, and the MMAs issued are waited for before
 // tensor memory is released.
 #include <cuda.h>
@@ -34,6 +40,9 @@
 namespace wq {
 namespace {
 
+#ifndef P2
+#define P2 32
+#endif
 constexpr int kTile = 128;      // tokens of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;  // how far (base 2) a score may pass m before m moves
@@ -50,6 +59,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+// Waits for this thread's loads from tensor memory; r's values are theirs only from here on.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -68,14 +87,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if (elect_one())
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if (elect_one()) mma_bf16_ts(d_tmem, a_tmem, b_desc, idesc, accumulate);   // the types are the descriptor's
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  if (elect_one()) tc_commit(bar);
 }
 // Instruction descriptor, kind::f16: fp32 accumulator, fp16 A (K-major) and B (K-major, or with its N
 // dimension contiguous).
@@ -186,7 +219,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
   uint64_t* drain = done + 1;           // the MMA issuer's last commit, after an abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-  const int warp = (int)warp_id(), lane = (int)lane_id();
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)warp_id(), 0), lane = (int)lane_id();   // known to be one for the warp
 
   // Which rows: the last row tiles of a sequence, which see most, first.
   uint32_t x = blockIdx.x;
@@ -303,20 +336,28 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
           if (first > 0) bits = first >= 32 ? 0u : bits & ~((1u << first) - 1u);
           return bits & ~flags[c >> 5].x;
         };
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(s_at + c, v);
-          tc_wait_ld();
+        // Loops are kept short (the roles share the instruction caches) and chains apart (four maxima, four sums).
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t v[2][32];
+          tmem_ld32(s_at + c, v[0]);
+          tmem_ld32(s_at + c + 32, v[1]);
+          wait_ld(v[0]);
+          wait_ld(v[1]);
           if (masked) {
-            const uint32_t see = sees(c);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : 0xFF800000u;
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t see = sees(c + 32 * u);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[u][k] = (see >> k) & 1u ? v[u][k] : 0xFF800000u;
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          for (int k = 0; k < 64; k += 2)
+            tops[(k >> 1) & 3] = max3(tops[(k >> 1) & 3], __uint_as_float(v[k >> 5][k & 31]), __uint_as_float(v[k >> 5][(k & 31) + 1]));
         }
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top == -INFINITY ? top : top * fac;
         const bool move = top > m + kSlack || (m == -INFINITY && top > m);
         if (__any_sync(0xFFFFFFFFu, move)) {
@@ -326,11 +367,11 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
           if (j > 0) {
             if (!wait_all(&ofull[grp], (j - 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t v[32];
               tmem_ld32(o_at + c, v);
-              tc_wait_ld();
+              wait_ld(v);
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
               tmem_st32(o_at + c, v);
@@ -339,32 +380,30 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
           }
         }
         const float base = m == -INFINITY ? 0.0f : kUp - m;
-        float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t v[32], pk[16];
           tmem_ld32(s_at + c, v);
-          tc_wait_ld();
-          if (masked) {
+          wait_ld(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(ex2(fmaf(__uint_as_float(v[k]), fac, base)));
+          if (masked) {                 // not by the score alone: -inf times a scale of zero is no number
             const uint32_t see = sees(c);
             if (see & flags[c >> 5].y) l = __uint_as_float(0x7FC00000u);   // a value that is no number
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              v[k] = (see >> k) & 1u ? __float_as_uint(ex2(fmaf(__uint_as_float(v[k]), fac, base))) : 0u;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(ex2(fmaf(__uint_as_float(v[k]), fac, base)));
+            for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : 0u;
           }
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float e0 = __uint_as_float(v[2 * k]), e1 = __uint_as_float(v[2 * k + 1]);
-            sum0 += e0;
-            sum1 += e1;
+            sums[(2 * k) & 3] += e0;
+            sums[(2 * k + 1) & 3] += e1;
             pk[k] = pack_f16x2(e0, e1);
           }
           tmem_st16(s_at + (c >> 1), pk);
         }
-        l += sum0 + sum1;
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -395,7 +434,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       uint32_t u[32];
       if (computed) {
         tmem_ld32(o_at + c, u);
-        tc_wait_ld();
+        wait_ld(u);
       }
       if (!row_there) continue;
 #pragma unroll
@@ -505,8 +544,10 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       fetch(row, raw);
       row_next = locate(j + 2);
     }
-  } else if (lane == 0 && tiles > 0) {
+  } else if (tiles > 0) {
     // ---------------------------------------------------------------- MMA issuer
+    // The whole warp runs this, and one lane is elected at each instruction: addresses and descriptors then stay in
+    // uniform registers (moved there one by one from a single thread's, they cost more than the MMAs).
     constexpr uint32_t kS = idesc_f16(128, 128, false), kO = idesc_f16(128, D, true);
     const uint64_t qd = smem_desc(smem_u32(smem + L::Q_OFF), 16, 1024, 2);
     const uint64_t kd = smem_desc(smem_u32(smem + L::K_OFF), 16, 1024, 2);
@@ -516,37 +557,37 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t at = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2);
-        mma_f16_ss(tmem + g * 128, ad + at, bd + at, kS, k != 0 ? 1u : 0u);
+        mma_ss_one(tmem + g * 128, ad + at, bd + at, kS, k != 0 ? 1u : 0u);
       }
-      tc_commit(&sfull[g]);
+      commit_one(&sfull[g]);
     };
-    bool ok = mbar_wait(qfull, 0, abort_flag) && mbar_wait(&kfull[0], 0, abort_flag);
+    bool ok = wait_all(qfull, 0, abort_flag) && wait_all(&kfull[0], 0, abort_flag);
     if (ok) {
       tc_fence_after();
       for (int g = 0; g < groups; ++g) scores(g, 0);
-      tc_commit(&kempty[0]);
+      commit_one(&kempty[0]);
     }
     for (int j = 0; j < tiles && ok; ++j) {
       const int buf = j & 1;
       for (int g = 0; g < groups && ok; ++g) {
-        if (g == 0 && !mbar_wait(&vfull[buf], (j >> 1) & 1, abort_flag)) { ok = false; break; }
-        if (!mbar_wait(&pfull[g], j & 1, abort_flag)) { ok = false; break; }
+        if (g == 0 && !wait_all(&vfull[buf], (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (!wait_all(&pfull[g], j & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint64_t bd = vd + (uint64_t)(buf * L::TB >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)               // 16 tokens: 8 columns of P, 2 KB of V
-          mma_bf16_ts(tmem + GROUPS * 128 + g * D, tmem + g * 128 + 8 * k, bd + 128 * k, kO, (j | k) != 0 ? 1u : 0u);
-        tc_commit(&ofull[g]);
-        if (g == groups - 1) tc_commit(&vempty[buf]);
+          mma_ts_one(tmem + GROUPS * 128 + g * D, tmem + g * 128 + 8 * k, bd + 128 * k, kO, (j | k) != 0 ? 1u : 0u);
+        commit_one(&ofull[g]);
+        if (g == groups - 1) commit_one(&vempty[buf]);
         if (j + 1 < tiles) {
-          if (g == 0 && !mbar_wait(&kfull[buf ^ 1], ((j + 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (g == 0 && !wait_all(&kfull[buf ^ 1], ((j + 1) >> 1) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           scores(g, j + 1);
-          if (g == groups - 1) tc_commit(&kempty[buf ^ 1]);
+          if (g == groups - 1) commit_one(&kempty[buf ^ 1]);
         }
       }
     }
-    if (!ok || *abort_flag) tc_commit(drain);
+    if (!ok || *abort_flag) commit_one(drain);
   }
 
   // Teardown: every warp arrives, then the MMA warp releases tensor memory.  The softmax warps have seen
