@@ -31,9 +31,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;   // tiles in a warp's ring
 constexpr int kSms = 152;
-#ifndef TCROWS
-#define TCROWS 32
-#endif
+// More query rows than this per cached head go to the tensor-memory kernel, whose tile holds 128: at 40 rows (8 x 4 heads
+// of 128 over 4096 tokens) it takes 31 us and this one 41, at 32 rows (8 x 8 heads over 4000) 61 and 39.
+constexpr int64_t kFewRows = 32;
 // More registers a thread beat more warps: 4, 3 and 2 blocks of NT = 1 an SM read one sequence of 2^20 tokens at
 // 4.6, 5.6 and 5.3 TB/s.
 constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -792,52 +792,72 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   if (p.cluster > 1) cluster_sync();    // the others may still read this block's shared memory
 }
 
-// Joins the parts of a query row and head: a block per row, its warps over the parts, lanes over
-// the elements, then the warps in order.  Launched while the attention kernel runs; it waits for it.
-constexpr int kJoinWarps = 8;
-template <int D>
+// Joins the parts of a query row and head.  Few parts: a warp per row.  More than kFewParts: a block per row,
+// its warps over the parts, then the warps in order.  Lanes are over the elements.  Launched while the attention
+// kernel runs; it waits for it.
+constexpr int kJoinWarps = 8, kFewParts = 8;
+template <int D, bool FEW>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p, int tile_rows) {
+  constexpr int E = D / 32, kStep = FEW ? 1 : kJoinWarps;
   const AttendArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t id = blockIdx.x;        // (sequence, token, head)
+  const int64_t id = FEW ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;   // (sequence, token, head)
+  const bool there = id < a.batch * a.tokens * a.q_heads;
   const int64_t bi = id / a.q_heads, b = bi / a.tokens, i = bi - b * a.tokens;
   const int hq = (int)(id - bi * a.q_heads), h = hq / p.group;
   const int64_t r = i * p.group + (hq - h * p.group);
-  const int parts = i < kv::count_of(a.counts, b, a.tokens) ? p.parts : 0;
+  const int parts = there && i < kv::count_of(a.counts, b, a.tokens) ? p.parts : 0;
   const int64_t slot = ((b * a.kv.heads + h) * p.row_tiles + r / tile_rows) * p.parts * tile_rows + r % tile_rows;
-  __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
   griddep_wait();
-  float top = -INFINITY, sum = 0.0f, o[D / 32];
+  float top = -INFINITY, sum = 0.0f, o[E];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
   for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_ml[2 * (slot + (int64_t)s * tile_rows)]);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll 4
-  for (int s = warp; s < parts; s += kJoinWarps) {
+  for (int s = FEW ? 0 : warp; s < parts; s += kStep) {
     const int64_t at = slot + (int64_t)s * tile_rows;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
     const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
     sum = fmaf(ml.y, f, sum);
+    float v[E];
+    if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p.part_o + at * D + E * lane);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p.part_o + at * D + E * lane);
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, p.part_o[at * D + 32 * e + lane], o[e]);
+    for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[e], o[e]);
   }
+  if (!FEW) {
+    __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) so[warp][32 * e + lane] = o[e];
-  if (lane == 0) sl[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  sum = 0.0f;
-  float v = 0.0f;
+    for (int e = 0; e < E; ++e) so[warp][E * lane + e] = o[e];
+    if (lane == 0) sl[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    sum = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    sum += sl[w];
-    v += so[w][threadIdx.x];
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      sum += sl[w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += so[w][E * lane + e];
+    }
   }
+  if (!there) return;
   const bool some = sum != 0.0f;
-  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head + threadIdx.x;
-  put(a, at, some ? v * (1.0f / sum) : 0.0f);
-  if (a.lse && threadIdx.x == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  const float inv = some ? 1.0f / sum : 0.0f;
+  const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = some ? o[e] * inv : 0.0f;
+  if (E == 4) {
+    put4(a, at, make_float4(o[0], o[1], o[2 % E], o[3 % E]));
+  } else if (a.f32) {
+    *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out.p) + at) = make_float2(o[0], o[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.p) + at) = pack_bf16x2(o[0], o[1]);
+  }
+  if (a.lse && lane == 0) a.lse[id] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 struct Plan {
@@ -853,7 +873,7 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   // The window only ever lowers the number of parts, so that the workspace without it suffices.
   const int64_t held = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
   const int64_t seen = window > 0 && window + tokens < held ? window + tokens : held;
-  pl.tc = rows > TCROWS;
+  pl.tc = rows > kFewRows;
   if (pl.tc) {
     // two groups of rows a block where that leaves a block for every SM; tokens are shared where it does not,
     // four tiles of 128 to a part at least
@@ -885,7 +905,8 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
 
 template <int D>
 int launch_join(const Params& p, int tile_rows, cudaStream_t s) {
-  const int64_t blocks = p.a.batch * p.a.tokens * p.a.q_heads;
+  const bool few = p.parts <= kFewParts;
+  const int64_t rows = p.a.batch * p.a.tokens * p.a.q_heads, blocks = few ? (rows + kJoinWarps - 1) / kJoinWarps : rows;
   if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
   cudaLaunchConfig_t jc{};
   jc.gridDim = dim3((unsigned)blocks);
@@ -896,7 +917,8 @@ int launch_join(const Params& p, int tile_rows, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   jc.attrs = at;
   jc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&jc, join_kernel<D>, p, tile_rows) != cudaSuccess) return WQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&jc, few ? join_kernel<D, true> : join_kernel<D, false>, p, tile_rows) != cudaSuccess)
+    return WQ_ERR_CUDA;
   count_launch();
   return WQ_OK;
 }

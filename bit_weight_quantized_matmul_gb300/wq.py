@@ -291,6 +291,8 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
 
 
 _pack_heads = struct.Struct("Pqqq").pack
+_kv_append, _kv_read = lib.wq_kv_append, lib.wq_kv_read
+_attend, _attend_workspace = lib.wq_attend, lib.wq_attend_workspace_bytes
 
 
 def _heads(t, dtype):
@@ -312,9 +314,10 @@ def kv_append(cache, k, v, start=None, counts=None, stream=None):
     of the cache (int32 CUDA tensors; None: 0, and all tokens)."""
     batch, tokens, heads, dim = k.shape
     assert v.shape == k.shape and heads == cache.heads and dim == cache.dim and batch <= cache.batch
-    _check("wq_kv_append", lib.wq_kv_append(cache.ref, _heads(k, torch.bfloat16),
-                                            _heads(v, torch.bfloat16), batch, tokens,
-                                            _index(start, batch), _index(counts, batch), _stream(stream)))
+    rc = _kv_append(cache.ref, _heads(k, torch.bfloat16), _heads(v, torch.bfloat16), batch, tokens,
+                    _index(start, batch), _index(counts, batch), _stream(stream))
+    if rc:
+        raise WQError("wq_kv_append", rc)
 
 
 def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, stream=None):
@@ -327,9 +330,10 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     dt = torch.float32 if out_f32 else torch.bfloat16
     k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
     v = torch.empty_like(k)
-    _check("wq_kv_read", lib.wq_kv_read(cache.ref, _heads(k, dt), _heads(v, dt), batch, tokens,
-                                        _index(start, batch), _index(counts, batch), WQ_FLAG_OUT_F32 if out_f32 else 0,
-                                        _stream(stream)))
+    rc = _kv_read(cache.ref, _heads(k, dt), _heads(v, dt), batch, tokens, _index(start, batch), _index(counts, batch),
+                  WQ_FLAG_OUT_F32 if out_f32 else 0, _stream(stream))
+    if rc:
+        raise WQError("wq_kv_read", rc)
     return k, v
 
 
@@ -351,22 +355,23 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
     assert dim == cache.dim and batch <= cache.batch
     dt = torch.float32 if out_f32 else torch.bfloat16
     if out is None:
-        out = torch.empty((batch, tokens, q_heads, dim), dtype=dt, device=q.device)
-    assert out.shape == q.shape
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+    else:
+        assert out.shape == q.shape
     lse = torch.empty((batch, tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
-        need = lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len)
+        need = _attend_workspace(cache.ref, batch, tokens, q_heads, max_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             if stream is not None:
                 workspace.record_stream(stream)
-    _check("wq_attend", lib.wq_attend(cache.ref, _heads(q, torch.bfloat16), _heads(out, dt),
-                                      None if lse is None else lse.data_ptr(), batch, tokens, q_heads,
-                                      _index(lens, batch), _index(counts, batch), max_len,
-                                      dim ** -0.5 if scale is None else scale, window,
-                                      (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
-                                      None if workspace is None else workspace.data_ptr(),
-                                      0 if workspace is None else workspace.numel(), _stream(stream)))
+    rc = _attend(cache.ref, _heads(q, torch.bfloat16), _heads(out, dt), None if lse is None else lse.data_ptr(), batch,
+                 tokens, q_heads, _index(lens, batch), _index(counts, batch), max_len, dim ** -0.5 if scale is None else scale,
+                 window, (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
+                 None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+                 _stream(stream))
+    if rc:
+        raise WQError("wq_attend", rc)
     return (out, lse) if return_lse else out
 
 
