@@ -22,11 +22,12 @@
 // A V scale that is no finite number cannot be left to the product (0 * NaN spoils rows that do not see
 // the token): the block is stored as zeros and the rows that do see the token are made NaN.
 //
-// Measured on GB300 (2 x 8 heads of 128 x 128 tokens of a group of 2, 19 sequences of 16384, one block an SM): 1075 TFLOP/s
-// (q4_0), 1130 (NVFP4), 0.56 and 0.59 of the measured bf16 rate; a tile of 128 tokens takes 4500 cycles, of which
-// a row's softmax 2300 and the tensor cores' work for its group 1100 follow one another.  Tried and slower: half
-// tiles of 64 tokens with scores ahead of the products (more, smaller MMAs: 815 TFLOP/s); one pass over S with
-// P kept in registers (915); a row's 128 scores in registers (spills).
+// Measured on GB300 (19 sequences of 16384 tokens, 8 cached heads of 128, 256 rows each, one block an SM): 1114
+// TFLOP/s (q4_0), 1177 (NVFP4), 0.58 and 0.61 of the measured bf16 rate.  Bound by a chain: a tile of 128 tokens
+// takes 4400 cycles, of which a row's softmax takes 2300 and its group's two products 1100, and the other group
+// has the tensor cores meanwhile.  Tried and slower: half tiles of 64 tokens with scores ahead of the
+// products (more, smaller MMAs: 815 TFLOP/s), one pass over S with P kept in registers (915), two threads a row (970),
+// a row's 128 scores in registers (spills), the codes of two tiles in registers (1118 / 1150).
 //
 // Every wait is bounded; after one ran out the roles stop, and the MMAs issued are waited for before
 // tensor memory is released.
@@ -143,6 +144,23 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Pairs of fp32 in one register pair, and operations on both, each rounded as by itself.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -380,14 +398,20 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
           }
         }
         const float base = m == -INFINITY ? 0.0f : kUp - m;
-        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t fac2 = two(fac, fac), base2 = two(base, base);
+        uint64_t sums[2] = {0, 0};      // two pairs of fp32 zeros
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t v[32], pk[16];
           tmem_ld32(s_at + c, v);
           wait_ld(v);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(ex2(fmaf(__uint_as_float(v[k]), fac, base)));
+          for (int k = 0; k < 32; k += 2) {
+            float e0, e1;
+            split(fma2f(two(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), fac2, base2), e0, e1);
+            v[k] = __float_as_uint(ex2(e0));
+            v[k + 1] = __float_as_uint(ex2(e1));
+          }
           if (masked) {                 // not by the score alone: -inf times a scale of zero is no number
             const uint32_t see = sees(c);
             if (see & flags[c >> 5].y) l = __uint_as_float(0x7FC00000u);   // a value that is no number
@@ -397,13 +421,14 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float e0 = __uint_as_float(v[2 * k]), e1 = __uint_as_float(v[2 * k + 1]);
-            sums[(2 * k) & 3] += e0;
-            sums[(2 * k + 1) & 3] += e1;
+            sums[k & 1] = add2f(sums[k & 1], two(e0, e1));
             pk[k] = pack_f16x2(e0, e1);
           }
           tmem_st16(s_at + (c >> 1), pk);
         }
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        float even, odd_sum;
+        split(add2f(sums[0], sums[1]), even, odd_sum);
+        l += even + odd_sum;
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
