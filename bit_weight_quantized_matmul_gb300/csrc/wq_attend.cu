@@ -110,22 +110,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// c - 8 of the codes in bits 0 .. 3 and 4 .. 7 of each half, as fp16 pairs: 1024 + c - 1032, and
-// (1024 + 16 c) / 16 - 72, both exact.
-__device__ __forceinline__ void signed_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = add2((w & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-  hi = fma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -599,8 +583,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
         for (int hf = 0; hf < 2; ++hf) {
           const uint32_t w = vw[hf][blk];
           if (FMT == WQ_Q4_0) {
-            signed_pairs(w, av[hf][0], av[hf][1]);
-            signed_pairs(w >> 8, av[hf][2], av[hf][3]);
+            kv::signed_pairs(w, av[hf][0], av[hf][1]);
+            kv::signed_pairs(w >> 8, av[hf][2], av[hf][3]);
           } else {
             // pairs of elements 0, 1 and 2, 3 of token 2q, then of token 2q + 1
             uint32_t r[4];

@@ -12,9 +12,12 @@
 namespace wq {
 namespace {
 
-// Small blocks and many of them beat large ones: 16 x 1500 tokens of 20 heads of 64 (q4_0) appended / read in
-// 47 / 37 us, against 53 / 52 us with blocks of 256 at 64 registers.
+// Small blocks and many of them beat large ones: 16 x 1500 tokens of 20 heads of 64 (q4_0) are appended in 47 us
+// (3.3 TB/s of 6.8 for a copy) and read in 31 (5.0 TB/s); blocks of 256 at 64 registers appended in 53, and read
+// in 52 where the small ones, with the decode of that time, took 37.
 constexpr int kThreads = 128, kUnroll = 4, kMinBlocks = 12;
+// NVFP4's divisions need the registers (4 x 2048 tokens of 8 heads of 128: 12.3 us, 12.8 at 12 blocks).
+constexpr int append_blocks(int fmt) { return fmt == WQ_Q4_0 ? 12 : 8; }
 
 __device__ __forceinline__ void widen8(const uint32_t (&u)[4], float (&x)[8]) {
 #pragma unroll
@@ -133,7 +136,7 @@ struct Rows {
 // sequence (blockIdx.z): blockIdx.x counts heads within chunks of tokens, so that neighbouring blocks
 // read or write neighbouring bf16 rows, and a block's codes are contiguous within a page.
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const __grid_constant__ KvMoveArgs a, const int wide) {
+__global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel(const __grid_constant__ KvMoveArgs a, const int wide) {
   constexpr int kPer = D / 8;           // threads a token
   const int which = blockIdx.y, chunk = blockIdx.x / (unsigned)a.kv.heads, h = blockIdx.x - chunk * a.kv.heads;
   const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8, i0 = chunk * wide * kUnroll;
@@ -188,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __g
     const int n = kv::count_of(a.counts, b, a.tokens);
     const int64_t start = kv::first_of(a.start, b);
     const float g = FMT == WQ_NVFP4 && a.kv.g[which] ? *a.kv.g[which] : 1.0f;
-    uint32_t w[kUnroll];
-    float sc[kUnroll];
+    const int64_t base = b * a.x[which].batch + h * a.x[which].head + e;
+    uint32_t w[kUnroll], sc[kUnroll];
     Rows rows;
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int i = i0 + k * wide + tok;
       w[k] = FMT == WQ_Q4_0 ? 0x88888888u : 0u;    // a row that is not there reads as zero
-      sc[k] = 0.0f;
+      sc[k] = 0u;
       const int64_t row = i < n ? rows.at(a.kv, b, start + i, h, k * wide) : -1;
       if (row >= 0) {
         w[k] = *reinterpret_cast<const uint32_t*>(a.kv.codes[which] + row * (D / 2) + e / 2);
@@ -207,8 +210,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __g
       const int i = i0 + k * wide + tok;
       if (i >= a.tokens) break;
       float v[8];
-      kv::decode8<FMT>(w[k], sc[k], g, v);
-      const int64_t at = b * a.x[which].batch + i * a.x[which].token + h * a.x[which].head + e;
+      if (FMT == WQ_Q4_0) kv::decode8<FMT>(w[k], 0u, f16_bits_to_f32(sc[k]), v);
+      else kv::decode8<FMT>(w[k], kv::e4m3_pair(sc[k]), g, v);
+      const int64_t at = base + i * a.x[which].token;
       if (F32) {
         float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.x[which].p) + at);
         dst[0] = make_float4(v[0], v[1], v[2], v[3]);

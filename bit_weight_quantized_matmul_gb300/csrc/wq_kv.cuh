@@ -65,28 +65,42 @@ __device__ __forceinline__ int count_of(const int32_t* counts, int64_t b, int64_
   return counts ? min(max(counts[b], 0), (int)tokens) : (int)tokens;
 }
 
-// The eight values of a 32-bit word of codes (element i in bits 4i .. 4i + 3).  q4_0: (c - 8) * d.
-// NVFP4: (E2M1(c) * s) * g, the inner product exact.
+// c - 8 of the q4_0 codes in bits 0 .. 3 and 4 .. 7 of each half, as fp16 pairs: 1024 + c - 1032, and
+// (1024 + 16 c) / 16 - 72, both exact.
+__device__ __forceinline__ void signed_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0xE408E408u));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"((w & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+}
+
+// The eight values of a 32-bit word of codes (element i in bits 4i .. 4i + 3).  q4_0: (c - 8) * s, s its d.
+// NVFP4: (E2M1(c) * E4M3) * s, the inner product exact in fp16 (pair: the block's scale in both halves), s its g.
 template <int FMT>
-__device__ __forceinline__ void decode8(uint32_t w, float s, float g, float (&v)[8]) {
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t pair, float s, float (&v)[8]) {
+  uint32_t r[4];
   if (FMT == WQ_Q4_0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn((float)((int)((w >> (4 * i)) & 15u) - 8), s);
+    signed_pairs(w, r[0], r[1]);
+    signed_pairs(w >> 8, r[2], r[3]);
   } else {
-    uint32_t r[4];
     e2m1_pairs(w, r);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __fmul_rn(__fmul_rn(f16_bits_to_f32(r[i] & 0xFFFFu), s), g);
-      v[2 * i + 1] = __fmul_rn(__fmul_rn(f16_bits_to_f32(r[i] >> 16), s), g);
-    }
+  for (int i = 0; i < 4; ++i) {
+    if (FMT == WQ_NVFP4) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(pair));
+    const int lo = FMT == WQ_Q4_0 ? i : 2 * i, hi = FMT == WQ_Q4_0 ? i + 4 : 2 * i + 1;
+    v[lo] = __fmul_rn(f16_bits_to_f32(r[i] & 0xFFFFu), s);
+    v[hi] = __fmul_rn(f16_bits_to_f32(r[i] >> 16), s);
   }
 }
-// Scale of element e of the row whose scale bytes start at p.
+// The scale bits of element e of the row whose scale bytes start at p.
 template <int FMT>
-__device__ __forceinline__ float scale_at(const uint8_t* p, int e) {
-  if (FMT == WQ_Q4_0) return f16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[e / 32]);
-  return e4m3_to_f32(p[e / 16]);
+__device__ __forceinline__ uint32_t scale_at(const uint8_t* p, int e) {
+  return FMT == WQ_Q4_0 ? reinterpret_cast<const uint16_t*>(p)[e / 32] : p[e / 16];
+}
+// An E4M3 byte as an fp16 pair of equals.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(b * 0x0101u));
+  return r;
 }
 
 }  // namespace kv
