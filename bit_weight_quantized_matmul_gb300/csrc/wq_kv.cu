@@ -2,7 +2,7 @@
 //
 // Both move each element once; HBM bounds them (append: 2 bytes in, 9/16 out; read the other way
 // round), and the launch a call of few tokens.  A thread owns the same eight elements of a head in up to
-// kUnroll tokens of one sequence, whose loads are in flight together: one 16-byte access on the bf16 side,
+// eight tokens of one sequence, whose loads are in flight together: one 16-byte access on the bf16 side,
 // four bytes of codes.  A q4_0 block is then four neighbouring lanes, an NVFP4 block two, and the
 // block's scale a maximum over them.
 #include <cuda_runtime.h>
@@ -12,10 +12,11 @@
 namespace wq {
 namespace {
 
-// Small blocks and many of them beat large ones: 16 x 1500 tokens of 20 heads of 64 (q4_0) are appended in 47 us
-// (3.3 TB/s of 6.8 for a copy) and read in 31 (5.0 TB/s); blocks of 256 at 64 registers appended in 53, and read
-// in 52 where the small ones, with the decode of that time, took 37.
-constexpr int kThreads = 128, kUnroll = 4, kMinBlocks = 12;
+// Small blocks and many of them, of as many rounds as their registers hold: each round's loads are in flight
+// together, and a block's beginning costs as much as two rounds.  8 x 1700 .. 2000 tokens of 20 heads of 64 in pages
+// of 64 (q4_0) are appended in 24 us (4.0 TB/s) and read in 18 (5.3); with 2 rounds in 30 and 26, with 8 and 4 in 35
+// and 19; at 8 blocks an SM in 26 and 21.
+constexpr int kThreads = 128, kAppendRounds = 4, kReadRounds = 8, kMinBlocks = 12;
 // NVFP4's divisions need the registers (4 x 2048 tokens of 8 heads of 128: 12.3 us, 12.8 at 12 blocks).
 constexpr int append_blocks(int fmt) { return fmt == WQ_Q4_0 ? 12 : 8; }
 
@@ -197,16 +198,16 @@ __device__ __forceinline__ void store_scale(uint8_t* row, int e, uint32_t scale)
   }
 }
 
-// A block covers one head of K (blockIdx.y 0) or V in kUnroll rounds of `wide` neighbouring tokens of one
+// A block covers one head of K (blockIdx.y 0) or V in some rounds of `wide` neighbouring tokens of one
 // sequence (blockIdx.z): blockIdx.x counts heads within chunks of tokens, so that neighbouring blocks
 // read or write neighbouring bf16 rows, and a block's codes are contiguous within a page.  In a paged cache the
 // chunks begin at positions that are multiples of their length, so that a round of a whole block never leaves its
 // page: the block looks up one row a round, or one in all.  Blocks at the ends, and calls of few tokens, look up
 // each token.  (16 x 1500 tokens of 20 heads of 64 in one slab each: a look-up per token took 42 us to append and
-// 31 to read, one per block 34 and 25.)
-template <int D>
+// 31 to read, one per block 34 and 23.)
+template <int D, int ROUNDS>
 struct Split {
-  static constexpr int kPer = D / 8, kWide = kThreads / kPer, kSpan = kWide * kUnroll;   // threads a token; tokens a round, a block
+  static constexpr int kPer = D / 8, kWide = kThreads / kPer, kSpan = kWide * ROUNDS;   // threads a token; tokens a round, a block
   // Tokens by which the first chunk begins before the call's first.
   static __device__ __forceinline__ int lead(const KvMoveArgs& a, int wide, int64_t start) {
     return wide == kWide && a.kv.table ? (int)(start & (kSpan - 1)) : 0;
@@ -229,18 +230,18 @@ struct Place {
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel(const __grid_constant__ KvMoveArgs a, const int wide) {
-  constexpr int kPer = Split<D>::kPer, kWide = Split<D>::kWide, kSpan = Split<D>::kSpan;
+  constexpr int kPer = Split<D, kAppendRounds>::kPer, kWide = Split<D, kAppendRounds>::kWide, kSpan = Split<D, kAppendRounds>::kSpan;
   const int which = blockIdx.y, chunk = blockIdx.x / (unsigned)a.kv.heads, h = blockIdx.x - chunk * a.kv.heads;
   const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8;
   for (int64_t b = blockIdx.z; b < a.batch; b += gridDim.z) {
     const int64_t start = kv::first_of(a.start, b), step = a.x[which].token;
-    const int64_t i0 = (int64_t)chunk * (wide * kUnroll) - Split<D>::lead(a, wide, start);
+    const int64_t i0 = (int64_t)chunk * (wide * kAppendRounds) - Split<D, kAppendRounds>::lead(a, wide, start);
     const int64_t rest = kv::count_of(a.counts, b, a.tokens) - i0;   // tokens from i0 on
     if (rest <= 0) continue;
     const float g = FMT == WQ_NVFP4 && a.kv.g[which] ? *a.kv.g[which] : 1.0f;
     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.x[which].p) + b * a.x[which].batch + h * a.x[which].head +
                           (i0 + tok) * step + e;
-    uint4 u[kUnroll];
+    uint4 u[kAppendRounds];
     const auto store = [&](int k, bool there, Place<D> p) {     // all lanes
       uint32_t sc;
       const uint32_t w = encode8<FMT>(u[k], g, sc);
@@ -250,17 +251,17 @@ __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel
     };
     if (wide == kWide && i0 >= 0 && rest >= kSpan) {
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) u[k] = *reinterpret_cast<const uint4*>(src + k * kWide * step);
+      for (int k = 0; k < kAppendRounds; ++k) u[k] = *reinterpret_cast<const uint4*>(src + k * kWide * step);
       int left;
       const int64_t row = kv::row_of(a.kv, b, start + i0, h, &left);
       if (row >= 0 && left >= kSpan) {
         const Place<D> first(a.kv, which, row + tok, e);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) store(k, true, first.ahead(k * kWide));
+        for (int k = 0; k < kAppendRounds; ++k) store(k, true, first.ahead(k * kWide));
       } else {
-        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % kUnroll) * kWide, h);   // lane k: round k's
+        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % kAppendRounds) * kWide, h);   // lane k: round k's
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kAppendRounds; ++k) {
           const int64_t r = __shfl_sync(0xFFFFFFFFu, mine, k);
           store(k, r >= 0, Place<D>(a.kv, which, r + tok, e));
         }
@@ -269,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel
     }
     const auto in = [&](int k) { return tok < wide && i0 + k * wide + tok >= 0 && k * wide + tok < rest; };
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) u[k] = in(k) ? *reinterpret_cast<const uint4*>(src + k * wide * step) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kAppendRounds; ++k) u[k] = in(k) ? *reinterpret_cast<const uint4*>(src + k * wide * step) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kAppendRounds; ++k) {
       if (k * wide >= rest) break;       // for the whole block: its lanes exchange values
       const int64_t row = in(k) ? row_at(a, b, start + i0 + k * wide + tok, h) : -1;
       store(k, row >= 0, Place<D>(a.kv, which, row, e));
@@ -296,17 +297,17 @@ __device__ __forceinline__ void put8(void* p, int64_t at, uint32_t w, uint32_t s
 
 template <int FMT, int D, bool F32>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __grid_constant__ KvMoveArgs a, const int wide) {
-  constexpr int kPer = Split<D>::kPer, kWide = Split<D>::kWide, kSpan = Split<D>::kSpan;
+  constexpr int kPer = Split<D, kReadRounds>::kPer, kWide = Split<D, kReadRounds>::kWide, kSpan = Split<D, kReadRounds>::kSpan;
   const int which = a.x[0].p ? blockIdx.y : 1, chunk = blockIdx.x / (unsigned)a.kv.heads, h = blockIdx.x - chunk * a.kv.heads;
   const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8;
   if (tok >= wide) return;
   for (int64_t b = blockIdx.z; b < a.batch; b += gridDim.z) {
     const int64_t start = kv::first_of(a.start, b), step = a.x[which].token;
-    const int64_t i0 = (int64_t)chunk * (wide * kUnroll) - Split<D>::lead(a, wide, start);
+    const int64_t i0 = (int64_t)chunk * (wide * kReadRounds) - Split<D, kReadRounds>::lead(a, wide, start);
     const int64_t rest = kv::count_of(a.counts, b, a.tokens) - i0;   // held tokens from i0 on
     const float g = FMT == WQ_NVFP4 && a.kv.g[which] ? *a.kv.g[which] : 1.0f;
     const int64_t at = b * a.x[which].batch + h * a.x[which].head + (i0 + tok) * step + e;
-    uint32_t w[kUnroll], sc[kUnroll];
+    uint32_t w[kReadRounds], sc[kReadRounds];
     const auto load = [&](int k, bool there, Place<D> p) {
       w[k] = FMT == WQ_Q4_0 ? 0x88888888u : 0u;    // a row that is not there reads as zero
       sc[k] = 0u;
@@ -320,27 +321,27 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __g
       if (row >= 0 && left >= kSpan) {
         const Place<D> first(a.kv, which, row + tok, e);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) load(k, true, first.ahead(k * kWide));
+        for (int k = 0; k < kReadRounds; ++k) load(k, true, first.ahead(k * kWide));
       } else {
-        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % kUnroll) * kWide, h);   // lane k: round k's
+        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % kReadRounds) * kWide, h);   // lane k: round k's
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kReadRounds; ++k) {
           const int64_t r = __shfl_sync(0xFFFFFFFFu, mine, k);
           load(k, r >= 0, Place<D>(a.kv, which, r + tok, e));
         }
       }
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) put8<FMT, F32>(a.x[which].p, at + k * kWide * step, w[k], sc[k], g);
+      for (int k = 0; k < kReadRounds; ++k) put8<FMT, F32>(a.x[which].p, at + k * kWide * step, w[k], sc[k], g);
       continue;
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kReadRounds; ++k) {
       const int i = k * wide + tok;
       const int64_t row = i0 + i >= 0 && i < rest ? row_at(a, b, start + i0 + i, h) : -1;
       load(k, row >= 0, Place<D>(a.kv, which, row, e));
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kReadRounds; ++k) {
       const int64_t i = i0 + k * wide + tok;
       if (i >= 0 && i < a.tokens) put8<FMT, F32>(a.x[which].p, at + k * wide * step, w[k], sc[k], g);
     }
@@ -353,12 +354,12 @@ struct Grid {
   dim3 blocks, threads;
   bool ok;
 };
-Grid grid_for(const KvMoveArgs& a, int sides) {
+Grid grid_for(const KvMoveArgs& a, int sides, int rounds) {
   Grid g{};
   const int per = a.kv.dim / 8;
   g.wide = (int)(a.tokens < kThreads / per ? a.tokens : kThreads / per);
   g.threads = dim3((unsigned)((g.wide * per + 31) / 32 * 32));
-  const int64_t span = g.wide * kUnroll, lead = g.wide == kThreads / per && a.kv.table && a.start ? span - 1 : 0;
+  const int64_t span = g.wide * rounds, lead = g.wide == kThreads / per && a.kv.table && a.start ? span - 1 : 0;
   const int64_t chunks = (a.tokens + lead + span - 1) / span;
   g.ok = chunks * a.kv.heads <= 0x7FFFFFFF;
   g.blocks = dim3((unsigned)(chunks * a.kv.heads), (unsigned)sides, (unsigned)(a.batch < 65535 ? a.batch : 65535));
@@ -372,14 +373,14 @@ int launched() {
 
 template <int FMT, int D>
 int append_t(const KvMoveArgs& a, cudaStream_t s) {
-  const Grid g = grid_for(a, 2);
+  const Grid g = grid_for(a, 2, kAppendRounds);
   if (!g.ok) return WQ_ERR_SHAPE;
   kv_append_kernel<FMT, D><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
   return launched();
 }
 template <int FMT, int D>
 int read_t(const KvMoveArgs& a, cudaStream_t s) {
-  const Grid g = grid_for(a, (a.x[0].p ? 1 : 0) + (a.x[1].p ? 1 : 0));
+  const Grid g = grid_for(a, (a.x[0].p ? 1 : 0) + (a.x[1].p ? 1 : 0), kReadRounds);
   if (!g.ok) return WQ_ERR_SHAPE;
   if (a.f32) kv_read_kernel<FMT, D, true><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
   else kv_read_kernel<FMT, D, false><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
