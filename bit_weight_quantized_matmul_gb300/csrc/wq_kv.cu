@@ -200,9 +200,9 @@ __device__ __forceinline__ void store_scale(uint8_t* row, int e, uint32_t scale)
 
 // A block covers one head of K (blockIdx.y 0) or V in some rounds of `wide` neighbouring tokens of one
 // sequence (blockIdx.z): blockIdx.x counts heads within chunks of tokens, so that neighbouring blocks
-// read or write neighbouring bf16 rows, and a block's codes are contiguous within a page.  In a paged cache the
-// chunks begin at positions that are multiples of their length, so that a round of a whole block never leaves its
-// page: the block looks up one row a round, or one in all.  Blocks at the ends, and calls of few tokens, look up
+// read or write neighbouring bf16 rows, and a block's codes are contiguous within a page.  The chunks
+// begin at positions that are multiples of their length, so that a round (8 or 16 tokens; a page's are a multiple of
+// 16) of a whole block never leaves its page: the block looks up one row a round, or one in all.  Blocks at the ends, and calls of few tokens, look up
 // each token.  (16 x 1500 tokens of 20 heads of 64 in one slab each: a look-up per token took 42 us to append and
 // 31 to read, one per block 34 and 23.)
 template <int D, int ROUNDS>
@@ -210,7 +210,7 @@ struct Split {
   static constexpr int kPer = D / 8, kWide = kThreads / kPer, kSpan = kWide * ROUNDS;   // threads a token; tokens a round, a block
   // Tokens by which the first chunk begins before the call's first.
   static __device__ __forceinline__ int lead(const KvMoveArgs& a, int wide, int64_t start) {
-    return wide == kWide && a.kv.table ? (int)(start & (kSpan - 1)) : 0;
+    return wide == kWide ? (int)(start & (kSpan - 1)) : 0;
   }
 };
 // Row of the token at position t, or -1 with the status set.
@@ -359,7 +359,7 @@ Grid grid_for(const KvMoveArgs& a, int sides, int rounds) {
   const int per = a.kv.dim / 8;
   g.wide = (int)(a.tokens < kThreads / per ? a.tokens : kThreads / per);
   g.threads = dim3((unsigned)((g.wide * per + 31) / 32 * 32));
-  const int64_t span = g.wide * rounds, lead = g.wide == kThreads / per && a.kv.table && a.start ? span - 1 : 0;
+  const int64_t span = g.wide * rounds, lead = g.wide == kThreads / per && a.start ? span - 1 : 0;
   const int64_t chunks = (a.tokens + lead + span - 1) / span;
   g.ok = chunks * a.kv.heads <= 0x7FFFFFFF;
   g.blocks = dim3((unsigned)(chunks * a.kv.heads), (unsigned)sides, (unsigned)(a.batch < 65535 ? a.batch : 65535));
