@@ -854,7 +854,8 @@ struct Plan {
 Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, int64_t window) {
   Plan pl{};
   const int64_t group = q_heads / kv.heads, rows = tokens * group;
-  // The window only ever lowers the number of parts, so that the workspace without it suffices.
+  // The window only ever lowers the number of parts, so that the workspace without it suffices (parts of 2048 tokens
+  // are more tiles than `most` asks for, so a window that lowers `want` below 8 leaves clusters).
   const int64_t held = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
   const int64_t seen = window > 0 && window + tokens < held ? window + tokens : held;
   pl.tc = rows > kFewRows;
@@ -881,8 +882,13 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   const int64_t tiles = (seen + tile - 1) / tile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
   int64_t want = (int64_t)kSms * blocks_per_sm(pl.nt) / (blocks > 0 ? blocks : 1);
   if (want > most) want = most;
-  pl.cluster = want > 8 ? 1 : want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
-  pl.parts = want > 8 ? (int)want : 1;
+  // Clusters come in powers of two.  Where that leaves blocks unused, parts of at least 2048 tokens are worth the
+  // join kernel: five parts of 16000 tokens of 80 heads of 128 take 48 us and clusters of four 54, of 2000 tokens
+  // 14.6 and 13.3.  (More blocks than fit at once never paid: 128 heads x 16000 in clusters of two, parts of
+  // three, clusters of four: 74, 72, 75; 152 heads x 2000: 15, 18, 21.)
+  const bool uneven = want > 2 && (want & (want - 1)) != 0 && tiles * tile >= 2048 * want;
+  pl.cluster = want > 8 || uneven ? 1 : want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
+  pl.parts = want > 8 || uneven ? (int)want : 1;
   pl.slots = pl.parts > 1 ? (size_t)(blocks * pl.parts * 8 * pl.nt) : 0;
   return pl;
 }

@@ -41,9 +41,6 @@
 namespace wq {
 namespace {
 
-#ifndef P2
-#define P2 32
-#endif
 constexpr int kTile = 128;      // tokens of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;  // how far (base 2) a score may pass m before m moves

@@ -7,7 +7,7 @@ import torch
 
 from oracle import kv as OK
 from tests.gpu_common import need_gpu, wq
-from tests.test_gpu_kv_cache import Case, bf16, check_append, ints, raw
+from tests.test_gpu_kv_cache import Case, bf16, check_append, check_attend, ints, raw
 
 pytestmark = pytest.mark.gpu
 FMTS = pytest.mark.parametrize("fmt", ["q4_0", "nvfp4"])
@@ -73,3 +73,39 @@ def test_long_calls_that_leave_the_cache(fmt, D, page, first):
     got = m.kv_read(cache, tokens, ints(start), out_f32=True)
     assert m.last_device_status() == m.WQ_ERR_ARG
     assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+
+
+@FMTS
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_calls_on_another_stream(fmt, tokens):
+    """stream=: append, attend (with a workspace) and read run there and give what the current stream gives; results and
+    workspace come from memory that the current stream's pending work does not use."""
+    need_gpu()
+    m, case = wq(), Case(73, fmt, 2, 128, 2, 4000, 16)
+    cache = case.upload()
+    k, v, q = (bf16(case.rng, 2, tokens, h, 128).cuda() for h in (2, 2, 8))
+    lens = ints([4000, 3001])
+    start = lens - tokens
+    m.kv_append(cache, k, v, start)
+    want, want_lse = m.attend(cache, q, lens, return_lse=True)
+    wk, wv = m.kv_read(cache, 4000, counts=lens)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        for _ in range(20):
+            busy.fill_(1)              # the current stream still writes this memory when it is given back
+        del busy
+        m.kv_append(cache, k, v, start, stream=other)
+        out, lse = m.attend(cache, q, lens, return_lse=True, stream=other)
+        gk, gv = m.kv_read(cache, 4000, counts=lens, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(gk, wk) and torch.equal(gv, wv)
+    assert m.last_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,window", [("q4_0", 0), ("nvfp4", 0), ("q4_0", 300), ("nvfp4", 6300)])
+def test_attend_over_an_uneven_number_of_parts(fmt, window):
+    """152 heads of long sequences: three parts each, joined from the workspace."""
+    need_gpu()
+    check_attend(Case(74, fmt, 38, 64, 4, 6400, 64), 1, 38, [6400, 1, 100, 4001], window=window)
