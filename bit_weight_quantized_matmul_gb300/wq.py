@@ -324,6 +324,9 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     """The values at start[b] + i, i < counts[b], of each sequence -> k, v [batch, tokens, heads, dim] (bf16, or
     fp32 with out_f32); rows from counts[b] on are zero.  batch defaults to start's or counts' length, else the
     cache's number of sequences."""
+    if stream is not None:                     # its results are allocated on the stream that writes them
+        with torch.cuda.stream(stream):
+            return kv_read(cache, tokens, start, counts, out_f32, batch)
     if batch is None:
         batch = cache.batch if start is None and counts is None else (counts if start is None else start).numel()
     assert batch <= cache.batch
@@ -331,7 +334,7 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
     v = torch.empty_like(k)
     rc = _kv_read(cache.ref, _heads(k, dt), _heads(v, dt), batch, tokens, _index(start, batch), _index(counts, batch),
-                  WQ_FLAG_OUT_F32 if out_f32 else 0, _stream(stream))
+                  WQ_FLAG_OUT_F32 if out_f32 else 0, _stream())
     if rc:
         raise WQError("wq_kv_read", rc)
     return k, v
@@ -351,6 +354,9 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
     sequences).  out: a [batch, tokens, q_heads, dim] view to write to.  Returns out, or (out, lse) with
     lse fp32 [batch, tokens, q_heads].  Rows that see nothing give 0 and -inf.  workspace: a uint8 tensor of
     attend_workspace_bytes() bytes that no other call in flight uses; allocated for the call when None."""
+    if stream is not None:                     # results and workspace are allocated on the stream that uses them
+        with torch.cuda.stream(stream):
+            return attend(cache, q, lens, counts, causal, window, scale, max_len, out, out_f32, return_lse, workspace)
     batch, tokens, q_heads, dim = q.shape
     assert dim == cache.dim and batch <= cache.batch
     dt = torch.float32 if out_f32 else torch.bfloat16
@@ -363,13 +369,11 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
         need = _attend_workspace(cache.ref, batch, tokens, q_heads, max_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
     rc = _attend(cache.ref, _heads(q, torch.bfloat16), _heads(out, dt), None if lse is None else lse.data_ptr(), batch,
                  tokens, q_heads, _index(lens, batch), _index(counts, batch), max_len, dim ** -0.5 if scale is None else scale,
                  window, (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
                  None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-                 _stream(stream))
+                 _stream())
     if rc:
         raise WQError("wq_attend", rc)
     return (out, lse) if return_lse else out
