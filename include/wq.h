@@ -261,7 +261,8 @@ int wq_linear_grouped_ex(const wq_problem_ex* problems, int count, int fmt, unsi
  * sequence owns page b whole (a contiguous slab per sequence).  The capacity of a
  * sequence is table_ld * page_size, or page_size without a table.
  *
- * Rules: dim is 64 or 128; page_size is a multiple of 16; heads >= 1; codes and
+ * Rules: dim is 64 or 128; page_size is a multiple of 16, at most 2^30; heads >= 1;
+ * pages * heads * page_size < 2^35 (WQ_ERR_SHAPE otherwise); codes and
  * scales 16-byte aligned, k_g / v_g / table 4-byte aligned.  k_g / v_g are used by
  * WQ_NVFP4 only; NULL stands for 1.  The struct lives in HOST memory; its pointers
  * are device pointers.
@@ -330,7 +331,12 @@ int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, i
  * lse = -inf.  Cache contents past lens[b] are never used, whatever they hold.
  * max_len: what the caller knows on the host of lens (an upper bound, used to
  * plan the split of long sequences only; 0 stands for the capacity).
- * scale: finite.  Softmax statistics and sums are fp32.
+ * scale: finite.  Softmax statistics and sums are fp32; K, V and the weights enter
+ * the products with 11 significant bits.
+ * A NaN query, key or key scale makes the rows that see it NaN.  A V block whose scale
+ * is not finite makes its own elements of the rows that see the token non-finite, or,
+ * with more than 32 query rows per cached head (tokens * q_heads / heads), the
+ * whole of those rows NaN.  No other row is touched by either.
  *
  * workspace: wq_attend_workspace_bytes(...) bytes (16-byte aligned, no
  * initialisation; may be NULL where that is 0) that no other call in flight uses. */
