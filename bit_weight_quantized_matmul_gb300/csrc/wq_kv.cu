@@ -1,7 +1,9 @@
 // wq_kv.cu -- quantising rows into the 4-bit KV cache as they are written, and reading them back.
 //
-// Both move each element once; HBM bounds them (append: 2 bytes in, 9/16 out; read the other way
-// round), and the launch a call of few tokens.  A thread owns the same eight elements of a head in up to
+// Both move each element once (append: 2 bytes in, 9/16 out; read the other way round).  HBM bounds the reading (8 x
+// 12000 .. 16384 tokens of 8 heads of 128, NVFP4, to bf16: 103 us, 6.5 TB/s of 6.8 for a copy), instruction issue the
+// appending (16 x 1500 x 20 x 64, q4_0: 35 us, 4.5 TB/s; 132 instructions per eight elements, issued 85 % of the
+// time), the launch a call of few tokens.  A thread owns the same eight elements of a head in up to
 // eight tokens of one sequence, whose loads are in flight together: one 16-byte access on the bf16 side,
 // four bytes of codes.  A q4_0 block is then four neighbouring lanes, an NVFP4 block two, and the
 // block's scale a maximum over them.
@@ -16,7 +18,8 @@ namespace {
 // together, and a block's beginning costs as much as two rounds.  8 x 1700 .. 2000 tokens of 20 heads of 64 in pages
 // of 64 (q4_0) are appended in 24 us (4.0 TB/s) and read in 18 (5.3); with 2 rounds in 30 and 26, with 8 and 4 in 35
 // and 19; at 8 blocks an SM in 26 and 21.
-constexpr int kThreads = 128, kAppendRounds = 4, kReadRounds = 8, kMinBlocks = 12;
+constexpr int kThreads = 128, kAppendRounds = 4, kReadRounds = 8, kReadRoundsFew = 2;
+constexpr int kMinBlocks = 12, kSms = 152;
 // NVFP4's divisions need the registers (4 x 2048 tokens of 8 heads of 128: 12.3 us, 12.8 at 12 blocks).
 constexpr int append_blocks(int fmt) { return fmt == WQ_Q4_0 ? 12 : 8; }
 
@@ -295,19 +298,19 @@ __device__ __forceinline__ void put8(void* p, int64_t at, uint32_t w, uint32_t s
   }
 }
 
-template <int FMT, int D, bool F32>
+template <int FMT, int D, bool F32, int ROUNDS>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __grid_constant__ KvMoveArgs a, const int wide) {
-  constexpr int kPer = Split<D, kReadRounds>::kPer, kWide = Split<D, kReadRounds>::kWide, kSpan = Split<D, kReadRounds>::kSpan;
+  constexpr int kPer = Split<D, ROUNDS>::kPer, kWide = Split<D, ROUNDS>::kWide, kSpan = Split<D, ROUNDS>::kSpan;
   const int which = a.x[0].p ? blockIdx.y : 1, chunk = blockIdx.x / (unsigned)a.kv.heads, h = blockIdx.x - chunk * a.kv.heads;
   const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8;
   if (tok >= wide) return;
   for (int64_t b = blockIdx.z; b < a.batch; b += gridDim.z) {
     const int64_t start = kv::first_of(a.start, b), step = a.x[which].token;
-    const int64_t i0 = (int64_t)chunk * (wide * kReadRounds) - Split<D, kReadRounds>::lead(a, wide, start);
+    const int64_t i0 = (int64_t)chunk * (wide * ROUNDS) - Split<D, ROUNDS>::lead(a, wide, start);
     const int64_t rest = kv::count_of(a.counts, b, a.tokens) - i0;   // held tokens from i0 on
     const float g = FMT == WQ_NVFP4 && a.kv.g[which] ? *a.kv.g[which] : 1.0f;
     const int64_t at = b * a.x[which].batch + h * a.x[which].head + (i0 + tok) * step + e;
-    uint32_t w[kReadRounds], sc[kReadRounds];
+    uint32_t w[ROUNDS], sc[ROUNDS];
     const auto load = [&](int k, bool there, Place<D> p) {
       w[k] = FMT == WQ_Q4_0 ? 0x88888888u : 0u;    // a row that is not there reads as zero
       sc[k] = 0u;
@@ -321,27 +324,27 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_read_kernel(const __g
       if (row >= 0 && left >= kSpan) {
         const Place<D> first(a.kv, which, row + tok, e);
 #pragma unroll
-        for (int k = 0; k < kReadRounds; ++k) load(k, true, first.ahead(k * kWide));
+        for (int k = 0; k < ROUNDS; ++k) load(k, true, first.ahead(k * kWide));
       } else {
-        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % kReadRounds) * kWide, h);   // lane k: round k's
+        const int64_t mine = row_at(a, b, start + i0 + (threadIdx.x % ROUNDS) * kWide, h);   // lane k: round k's
 #pragma unroll
-        for (int k = 0; k < kReadRounds; ++k) {
+        for (int k = 0; k < ROUNDS; ++k) {
           const int64_t r = __shfl_sync(0xFFFFFFFFu, mine, k);
           load(k, r >= 0, Place<D>(a.kv, which, r + tok, e));
         }
       }
 #pragma unroll
-      for (int k = 0; k < kReadRounds; ++k) put8<FMT, F32>(a.x[which].p, at + k * kWide * step, w[k], sc[k], g);
+      for (int k = 0; k < ROUNDS; ++k) put8<FMT, F32>(a.x[which].p, at + k * kWide * step, w[k], sc[k], g);
       continue;
     }
 #pragma unroll
-    for (int k = 0; k < kReadRounds; ++k) {
+    for (int k = 0; k < ROUNDS; ++k) {
       const int i = k * wide + tok;
       const int64_t row = i0 + i >= 0 && i < rest ? row_at(a, b, start + i0 + i, h) : -1;
       load(k, row >= 0, Place<D>(a.kv, which, row, e));
     }
 #pragma unroll
-    for (int k = 0; k < kReadRounds; ++k) {
+    for (int k = 0; k < ROUNDS; ++k) {
       const int64_t i = i0 + k * wide + tok;
       if (i >= 0 && i < a.tokens) put8<FMT, F32>(a.x[which].p, at + k * wide * step, w[k], sc[k], g);
     }
@@ -378,13 +381,22 @@ int append_t(const KvMoveArgs& a, cudaStream_t s) {
   kv_append_kernel<FMT, D><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
   return launched();
 }
+template <int FMT, int D, int ROUNDS>
+int read_t(const KvMoveArgs& a, const Grid& g, cudaStream_t s) {
+  if (!g.ok) return WQ_ERR_SHAPE;
+  if (a.f32) kv_read_kernel<FMT, D, true, ROUNDS><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
+  else kv_read_kernel<FMT, D, false, ROUNDS><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
+  return launched();
+}
+// Fewer rounds a block where eight would leave half of the device's places empty: 3 x 777 tokens of 8 heads of 128 in
+// pages of 16 to fp32 take 8.0 us with eight rounds (624 blocks), 6.3 with two, 100 tokens 3.3 and 2.3; 2 x 2500 of 20
+// heads of 64 (1600 blocks) 6.1 and 8.9.
 template <int FMT, int D>
 int read_t(const KvMoveArgs& a, cudaStream_t s) {
-  const Grid g = grid_for(a, (a.x[0].p ? 1 : 0) + (a.x[1].p ? 1 : 0), kReadRounds);
-  if (!g.ok) return WQ_ERR_SHAPE;
-  if (a.f32) kv_read_kernel<FMT, D, true><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
-  else kv_read_kernel<FMT, D, false><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
-  return launched();
+  const int sides = (a.x[0].p ? 1 : 0) + (a.x[1].p ? 1 : 0);
+  const Grid g = grid_for(a, sides, kReadRounds);
+  if ((int64_t)g.blocks.x * g.blocks.y * g.blocks.z >= kSms * kMinBlocks / 2) return read_t<FMT, D, kReadRounds>(a, g, s);
+  return read_t<FMT, D, kReadRoundsFew>(a, grid_for(a, sides, kReadRoundsFew), s);
 }
 
 }  // namespace
