@@ -177,7 +177,7 @@ int check_cache(const wq_kv_cache* c, KvArgs& a) {
   a.heads = c->heads;
   a.dim = c->dim;
   a.capacity = c->table ? c->table_ld * c->page_size : c->page_size;
-  if (a.capacity > 0x7FFFFFF0) a.capacity = 0x7FFFFFF0;  // positions are int32
+  if (a.capacity > 0x7FFFFF00) a.capacity = 0x7FFFFF00;  // positions are int32, and whole tiles past them too
   return WQ_OK;
 }
 

@@ -259,7 +259,7 @@ int wq_linear_grouped_ex(const wq_problem_ex* problems, int count, int fmt, unsi
  * page_size, dim] of that format).  Position t of sequence b lies in page
  * table[b * table_ld + t / page_size] at t % page_size; with table == NULL the
  * sequence owns page b whole (a contiguous slab per sequence).  The capacity of a
- * sequence is table_ld * page_size, or page_size without a table.
+ * sequence is table_ld * page_size, or page_size without a table (and 2^31 - 256 at most).
  *
  * Rules: dim is 64 or 128; page_size is a multiple of 16, at most 2^30; heads >= 1;
  * pages * heads * page_size < 2^35 (WQ_ERR_SHAPE otherwise); codes and

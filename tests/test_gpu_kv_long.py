@@ -109,3 +109,26 @@ def test_attend_over_an_uneven_number_of_parts(fmt, window):
     """152 heads of long sequences: three parts each, joined from the workspace."""
     need_gpu()
     check_attend(Case(74, fmt, 38, 64, 4, 6400, 64), 1, 38, [6400, 1, 100, 4001], window=window)
+
+
+@FMTS
+@pytest.mark.parametrize("D,q_heads,tokens", [(64, 4, 1), (128, 16, 3), (64, 2, 40), (128, 16, 150)])
+def test_attend_leaves_out_pages_that_are_not_there(fmt, D, q_heads, tokens):
+    """Bad table entries in the middle of a sequence: its tokens are not there, the other sequence is untouched, the status
+    tells.  Bounds as for any attention."""
+    need_gpu()
+    m, case = wq(), Case(75, fmt, 2, D, 2, 640, 16)
+    lens = [633, 500]
+    kv = [case.values(b, lens[b]) for b in range(2)]
+    case.table[1, 3], case.table[1, 17] = -1, case.pages
+    there = np.ones(lens[1], bool)
+    there[48:64] = there[272:288] = False
+    kv[1] = [x[there] for x in kv[1]]
+    q = bf16(case.rng, 2, tokens, q_heads, D)
+    assert m.last_device_status() == 0
+    out, lse = m.attend(case.upload(), q.cuda(), ints(lens), out_f32=True, return_lse=True)
+    assert m.last_device_status() == m.WQ_ERR_ARG
+    for b in range(2):
+        ref, rlse, mean, top = OK.attend(q[b].float().numpy(), kv[b][0], kv[b][1], tokens, D ** -0.5, True)
+        assert np.all(np.abs(out[b].cpu().double().numpy() - ref) <= (2.0 ** -11 * (2 * top[..., None] + 4) + 2.0 ** -20) * mean + 1e-30)
+        assert np.all(np.abs(lse[b].cpu().double().numpy() - rlse) <= 2.0 ** -11 * top + 2.0 ** -20 * np.abs(rlse) + 2.0 ** -20)
