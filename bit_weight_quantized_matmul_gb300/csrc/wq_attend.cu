@@ -142,6 +142,8 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// The top bit of each half of an fp16 pair that is infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 // Which of a lane's eight elements of a block pair p of a K operand holds (see the K unpacking).
 template <int FMT>
 __device__ __forceinline__ constexpr int pair_lo(int p) { return FMT == WQ_Q4_0 ? p : 2 * p; }
@@ -584,6 +586,37 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
           }
         }
       }
+      // A weight of zero takes nothing from a finite scale only.  Here some row may not see a token, so a scale that is no
+      // finite number becomes zero, and the block's elements of the rows that do see the token become NaN.
+      if (masked) {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) odd |= not_finite(vs[0][blk]) | not_finite(vs[1][blk]);
+        if (__any_sync(0xFFFFFFFFu, odd != 0)) {
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            const uint32_t bad0 = not_finite(vs[0][blk]), bad1 = not_finite(vs[1][blk]);
+            bool hit[NT][2] = {};
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {    // token k of the group: its scale lies in lane (g, k / 2 % 4)
+              const uint32_t bad = __shfl_sync(0xFFFFFFFFu, k < 8 ? bad0 : bad1, (lane & ~3) | ((k >> 1) & 3));
+              const int t = tile * kTile + 16 * u + k;
+              if (!((bad >> (15 + 16 * (k & 1))) & 1u) || ((gone >> u) & 1u)) continue;
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) hit[j][c] |= t >= c_lo[j][c] && t < c_hi[j][c];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (hit[j][i & 1]) o[j][2 * blk + (i >> 2)][i & 3] = __uint_as_float(0x7FC00000u);
+            vs[0][blk] &= ~((bad0 >> 15) * 0xFFFFu);
+            vs[1][blk] &= ~((bad1 >> 15) * 0xFFFFu);
+          }
+        }
+      }
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
         uint32_t av[2][4];              // [tokens][element 4g + e of the block]
@@ -609,10 +642,6 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
           if (FMT == WQ_Q4_0) {
             b0 = mul2(b0, vs[0][blk]);
             b1 = mul2(b1, vs[1][blk]);
-            if (masked) {               // a weight of zero takes nothing from a scale that is no number
-              b0 = ((pb[j][0] & 0x7FFFu) ? b0 & 0xFFFFu : 0u) | ((pb[j][0] & 0x7FFF0000u) ? b0 & 0xFFFF0000u : 0u);
-              b1 = ((pb[j][1] & 0x7FFFu) ? b1 & 0xFFFFu : 0u) | ((pb[j][1] & 0x7FFF0000u) ? b1 & 0xFFFF0000u : 0u);
-            }
           }
           mma(o[j][2 * blk], av[0][0], av[0][1], av[1][0], av[1][1], b0, b1);
           mma(o[j][2 * blk + 1], av[0][2], av[0][3], av[1][2], av[1][3], b0, b1);
