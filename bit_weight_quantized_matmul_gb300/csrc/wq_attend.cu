@@ -16,9 +16,15 @@
 // the accumulator's initial value, -8 * sum(Q) over the block, and d multiplies the block's partial score in
 // fp32.  V: a nibble under the exponent of 1024 less 1032 is c - 8 (the sum over tokens runs over weights
 // that differ by many orders of magnitude, so an offset taken off afterwards would leave its rounding in
-// elements that are small); d multiplies the weight (p and p d are rounded to fp16, 2^-11 each).  NVFP4:
-// E2M1(c) * E4M3(s) is exact in fp16 (6 significant bits), g enters with the softmax scale and the output.
-// Q is scaled per row by a power of two, so that its bf16 values are exact in fp16.
+// elements that are small), times d, rounded to fp16: 2^-12 of a value of any size.  (d on the weight's side takes
+// six instructions less per 16 tokens and block, 0 to 2 % of the time, but p d leaves fp16's range for small d and
+// small p alike.)  NVFP4: E2M1(c) * E4M3(s) is exact in fp16 (6 significant bits), g enters with the softmax scale
+// and the output.  The weights p are rounded to fp16 as 2^kUp p: to 11 bits down to 2^-26 (q4_0) or 2^-29 (NVFP4)
+// of a row's largest.  Q is scaled per row by a power of two, so that its bf16 values are exact in fp16.
+//
+// A d that (c - 8) d may overflow with (|d| >= 8192) and scales of V that are no finite numbers are not looked for at
+// each tile, which took 3 %.  Either leaves O not finite; a warp that finds its O so goes through its tiles a second time,
+// with d / 8 and 8 p where d is large, and with such scales out of the product.
 //
 // Must read 0.5625 bytes an element of the visible K and V once.  Measured on GB300: one sequence of 2^20 tokens, 8 heads
 // of 128, 5.6 TB/s (q4_0) and 5.4 (NVFP4) of 6.8 for a copy; 57 x 8 heads x 4500 tokens (one block for every place on
@@ -142,8 +148,16 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// The top bit of each half of an fp16 pair that is infinite or NaN.
-__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+// The top bit of each scale in a word that is infinite or NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return FMT == WQ_Q4_0 ? ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u : ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+// The top bit of each half of an fp16 pair that is 8192 or more in magnitude (or no finite number).
+__device__ __forceinline__ uint32_t large(uint32_t x) { return ((x & 0x70007000u) + 0x10001000u) & 0x80008000u; }
+// For each half 1/8 (8) where it is large, else 1.
+__device__ __forceinline__ uint32_t eighth(uint32_t x) { return 0x3C003C00u - (large(x) >> 15) * 0x0C00u; }
+__device__ __forceinline__ uint32_t eightfold(uint32_t x) { return 0x3C003C00u + (large(x) >> 15) * 0x0C00u; }
 // Which of a lane's eight elements of a block pair p of a K operand holds (see the K unpacking).
 template <int FMT>
 __device__ __forceinline__ constexpr int pair_lo(int p) { return FMT == WQ_Q4_0 ? p : 2 * p; }
@@ -170,8 +184,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   constexpr int NB = D / 32;            // 32-element blocks of a row
   constexpr int kTile = tile_tokens(D, NT), kGroups = kTile / 16;   // 16 tokens lie in one page
   constexpr int kCodes = kTile * (D / 2), kScales = kTile * kv::scale_bytes(D);
-  // p = 2^(score - m + kUp): NVFP4's weights use fp16's upper range too (q4_0's are still to be multiplied by d)
-  constexpr float kUp = FMT == WQ_NVFP4 ? 15.0f : 0.0f;
+  // p = 2^(score - m + kUp): the weights use fp16's upper range too (q4_0's may still be multiplied by 8)
+  constexpr float kUp = FMT == WQ_NVFP4 ? 15.0f : 12.0f;
   constexpr bool kQSmem = NT > 2;       // Q fragments live in shared memory instead of registers
   extern __shared__ __align__(128) uint8_t smem[];
   const AttendArgs& a = p.a;
@@ -380,24 +394,61 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
     }
 
   float o[NT][2 * NB][4], m[NT][2], l[NT][2];
+  auto reset = [&] {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    m[j][0] = m[j][1] = -INFINITY;
-    l[j][0] = l[j][1] = 0.0f;
+    for (int j = 0; j < NT; ++j) {
+      m[j][0] = m[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int d = 0; d < 2 * NB; ++d) o[j][d][k] = 0.0f;
-  }
+        for (int d = 0; d < 2 * NB; ++d) o[j][d][k] = 0.0f;
+    }
+  };
+  reset();
 
   // ---------------------------------------------------------------- tiles
   // This lane's row address for ldmatrix: four blocks of eight tokens (D = 128), or two of sixteen.
   const uint32_t lane_at = D == 128 ? tile_at<D>(lane & 7, lane >> 3) : tile_at<D>(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
-  // One tile; masked: some row does not see all of it.
-  auto work = [&](auto masked_c, int tile, int stage, uint32_t gone) {
+  // A weight of zero takes nothing from a finite scale of V only.  Where some row does not see all of a tile, scales that
+  // are no finite numbers become zero, and their elements of the rows that do see the token become NaN.  sp: V's scales.
+  auto clean = [&](int tile, uint8_t* sp) {
+    uint2 w = make_uint2(0u, 0u);
+    if (kScales == 256 || lane < kScales / 8) w = *reinterpret_cast<const uint2*>(sp + 8 * lane);
+    const uint32_t bad0 = not_finite<FMT>(w.x), bad1 = not_finite<FMT>(w.y);
+    if (!__any_sync(0xFFFFFFFFu, (bad0 | bad1) != 0)) return;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      bool hit[NT][2] = {};
+#pragma unroll 1
+      for (int r = 0; r < kTile; ++r) {       // the scale of this lane's elements 4g .. 4g + 3 of the block
+        const uint8_t* at = sp + r * kv::scale_bytes(D) + 2 * blk;
+        const uint32_t sc = FMT == WQ_Q4_0 ? *reinterpret_cast<const uint16_t*>(at) : at[g >> 2];
+        const int t = tile * kTile + r;
+        if (not_finite<FMT>(sc) == 0) continue;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) hit[j][c] |= t >= c_lo[j][c] && t < c_hi[j][c];
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (hit[j][i & 1]) o[j][2 * blk + (i >> 2)][i & 3] = __uint_as_float(0x7FC00000u);
+    }
+    __syncwarp();
+    constexpr int kTop = FMT == WQ_Q4_0 ? 15 : 7;
+    constexpr uint32_t kAll = FMT == WQ_Q4_0 ? 0xFFFFu : 0xFFu;
+    if (bad0 | bad1) *reinterpret_cast<uint2*>(sp + 8 * lane) = make_uint2(w.x & ~((bad0 >> kTop) * kAll), w.y & ~((bad1 >> kTop) * kAll));
+    __syncwarp();
+  };
+  // One tile.  masked: some row does not see all of it, or (careful) V's scales are looked at.
+  auto work = [&](auto masked_c, bool careful, int tile, int stage, uint32_t gone) {
     constexpr bool masked = decltype(masked_c)::value;
     const uint32_t base = ring + stage * kStageBytes;
-    const uint8_t* gen = smem + (base - smem_u32(smem));
+    uint8_t* gen = smem + (base - smem_u32(smem));
+    if (masked && careful) clean(tile, gen + 2 * kCodes + kScales);
     // ---- scores, two groups at a time
     float s[kGroups][NT][4];
 #pragma unroll
@@ -586,37 +637,6 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
           }
         }
       }
-      // A weight of zero takes nothing from a finite scale only.  Here some row may not see a token, so a scale that is no
-      // finite number becomes zero, and the block's elements of the rows that do see the token become NaN.
-      if (masked) {
-        uint32_t odd = 0;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) odd |= not_finite(vs[0][blk]) | not_finite(vs[1][blk]);
-        if (__any_sync(0xFFFFFFFFu, odd != 0)) {
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            const uint32_t bad0 = not_finite(vs[0][blk]), bad1 = not_finite(vs[1][blk]);
-            bool hit[NT][2] = {};
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {    // token k of the group: its scale lies in lane (g, k / 2 % 4)
-              const uint32_t bad = __shfl_sync(0xFFFFFFFFu, k < 8 ? bad0 : bad1, (lane & ~3) | ((k >> 1) & 3));
-              const int t = tile * kTile + 16 * u + k;
-              if (!((bad >> (15 + 16 * (k & 1))) & 1u) || ((gone >> u) & 1u)) continue;
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) hit[j][c] |= t >= c_lo[j][c] && t < c_hi[j][c];
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (hit[j][i & 1]) o[j][2 * blk + (i >> 2)][i & 3] = __uint_as_float(0x7FC00000u);
-            vs[0][blk] &= ~((bad0 >> 15) * 0xFFFFu);
-            vs[1][blk] &= ~((bad1 >> 15) * 0xFFFFu);
-          }
-        }
-      }
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
         uint32_t av[2][4];              // [tokens][element 4g + e of the block]
@@ -626,6 +646,9 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
           if (FMT == WQ_Q4_0) {
             kv::signed_pairs(w, av[hf][0], av[hf][1]);
             kv::signed_pairs(w >> 8, av[hf][2], av[hf][3]);
+            const uint32_t d = masked && careful ? mul2(vs[hf][blk], eighth(vs[hf][blk])) : vs[hf][blk];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) av[hf][e] = mul2(av[hf][e], d);
           } else {
             // pairs of elements 0, 1 and 2, 3 of token 2q, then of token 2q + 1
             uint32_t r[4];
@@ -639,9 +662,9 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint32_t b0 = pb[j][0], b1 = pb[j][1];
-          if (FMT == WQ_Q4_0) {
-            b0 = mul2(b0, vs[0][blk]);
-            b1 = mul2(b1, vs[1][blk]);
+          if (FMT == WQ_Q4_0 && masked && careful) {
+            b0 = mul2(b0, eightfold(vs[0][blk]));
+            b1 = mul2(b1, eightfold(vs[1][blk]));
           }
           mma(o[j][2 * blk], av[0][0], av[0][1], av[1][0], av[1][1], b0, b1);
           mma(o[j][2 * blk + 1], av[0][2], av[0][3], av[1][2], av[1][3], b0, b1);
@@ -649,28 +672,54 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
       }
     }
   };
-  int stage = 0, from = (kStages - 1) * kGroups;
-  for (int tile = t_begin; tile < t_end; tile += kWarps) {
-    {
-      const int ahead = tile + (kStages - 1) * kWarps;
-      int s = stage + kStages - 1;
-      if (s >= kStages) s -= kStages;
-      if (from == 32) {                 // the next kSpan tiles' rows; those after them come in meanwhile
-        from = 0;
-        rows_now = rows_next;
-        rows_next = locate(ahead + kSpan * kWarps);
+  // Once a weight's product was not finite its sum in O stays so: then the warp goes through its tiles once more, carefully.
+  int from = (kStages - 1) * kGroups, start = t_begin;
+  for (bool careful = false;; careful = true) {
+    int stage = 0;
+    for (int tile = start; tile < t_end; tile += kWarps) {
+      {
+        const int ahead = tile + (kStages - 1) * kWarps;
+        int s = stage + kStages - 1;
+        if (s >= kStages) s -= kStages;
+        if (from == 32) {               // the next kSpan tiles' rows; those after them come in meanwhile
+          from = 0;
+          rows_now = rows_next;
+          rows_next = locate(ahead + kSpan * kWarps);
+        }
+        if (ahead < t_end) issue(ahead, s, rows_now, from);
+        from += kGroups;
+        cp_commit();
       }
-      if (ahead < t_end) issue(ahead, s, rows_now, from);
-      from += kGroups;
-      cp_commit();
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t gone = (missing >> (4 * stage)) & 15u;
+      if (careful || gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min) {
+        if (tile >= t_begin) work(std::true_type{}, careful, tile, stage, gone);
+      } else {
+        work(std::false_type{}, false, tile, stage, 0u);
+      }
+      if (++stage == kStages) stage = 0;
+      __syncwarp();                     // every lane has read the stage before it is filled again
     }
-    cp_wait<kStages - 1>();
+    if (careful) break;
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float z = 0.0f;                 // 0 times O, all added up
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d) z = fmaf(o[j][d][c], 0.0f, fmaf(o[j][d][c + 2], 0.0f, z));
+        odd |= z != 0.0f && r0 + 8 * j + 2 * q + c < rows;
+      }
+    if (!__any_sync(0xFFFFFFFFu, odd)) break;
+    reset();
+    cp_wait<0>();                       // the ring is empty; two rounds fill it again
     __syncwarp();
-    const uint32_t gone = (missing >> (4 * stage)) & 15u;
-    if (gone != 0 || tile * kTile < lo_max || (tile + 1) * kTile > hi_min) work(std::true_type{}, tile, stage, gone);
-    else work(std::false_type{}, tile, stage, 0u);
-    if (++stage == kStages) stage = 0;
-    __syncwarp();                       // every lane has read the stage before it is filled again
+    rows_now = locate(t_begin);
+    rows_next = locate(t_begin + kSpan * kWarps);
+    from = 0;
+    start = t_begin - (kStages - 1) * kWarps;
   }
   cp_wait<0>();
 

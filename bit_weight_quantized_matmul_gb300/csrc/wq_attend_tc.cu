@@ -14,10 +14,12 @@
 // ahead, fp16 rows in the 128-byte swizzle), one thread that issues the MMAs.  While one group's softmax
 // runs, the tensor cores work for the other; K and V are double-buffered.
 //
-// q4_0 rows hold (c - 8) d / 8 (at most 65504: no d overflows fp16), elements of an octet in the order
-// 0 4 1 5 2 6 3 7 in which masking a word of codes leaves them; Q's rows and O's columns follow it.  NVFP4
-// rows hold E2M1(c) E4M3(s), exact, and g enters with the softmax scale and the output.  Rounding K, V and P
-// to fp16's 11 bits is what this path costs in precision (2^-12 each, independent).
+// q4_0 rows hold (c - 8) d, elements of an octet in the order 0 4 1 5 2 6 3 7 in which masking a word of codes
+// leaves them; Q's rows and O's columns follow it.  Where |d| >= 8192 in some block could overflow fp16, the token's
+// whole row holds an eighth and is marked: the softmax takes its scores, or its weight in the product, eightfold.
+// NVFP4 rows hold E2M1(c) E4M3(s), exact, and g enters with the softmax scale and the output.  Rounding K, V and P
+// to fp16's 11 bits is what this path costs in precision (2^-12 each, independent; beside a block with |d| >= 8192,
+// 2^-22 in the values of the token's other blocks).
 //
 // A V scale that is no finite number cannot be left to the product (0 * NaN spoils rows that do not see
 // the token): the block is stored as zeros and the rows that do see the token are made NaN.
@@ -165,26 +167,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The top bit of each half of an fp16 pair that is 8192 or more, or no finite number.
+__device__ __forceinline__ uint32_t large(uint32_t x) { return ((x & 0x70007000u) + 0x10001000u) & 0x80008000u; }
 // Element of an octet that position e of an operand row holds.
 template <int FMT>
 __device__ __forceinline__ constexpr int octet(int e) { return FMT == WQ_Q4_0 ? (e & 1) * 4 + (e >> 1) : e; }
 
-// Eight codes -> eight fp16 values in operand order (q4_0: an eighth of them).  s: the block's scale in both halves.
+// Eight codes -> eight fp16 values in operand order (eighth, q4_0: an eighth of them).  s: the block's scale in both halves.
 template <int FMT>
-__device__ __forceinline__ uint4 operand8(uint32_t w, uint32_t s) {
+__device__ __forceinline__ uint4 operand8(uint32_t w, uint32_t s, bool eighth) {
   uint32_t r[4];
   if (FMT == WQ_Q4_0) {
-    // (c - 8) / 8: (1024 + c) / 8 - 129, and (1024 + 16 c) / 128 - 9, exact; times d one rounding
-    r[0] = fma2((w & 0x000F000Fu) | 0x64006400u, 0x30003000u, 0xD808D808u);
-    r[1] = fma2((w & 0x00F000F0u) | 0x64006400u, 0x20002000u, 0xC880C880u);
+    // c - 8 = (1024 + c) - 1032 and (1024 + 16 c) / 16 - 72, or (1024 + c) / 8 - 129 and (1024 + 16 c) / 128 - 9, exact
+    // (scaled here and not in s, which may have no bits to spare); times s one rounding
+    const uint32_t m0 = eighth ? 0x30003000u : 0x3C003C00u, c0 = eighth ? 0xD808D808u : 0xE408E408u;
+    const uint32_t m1 = eighth ? 0x20002000u : 0x2C002C00u, c1 = eighth ? 0xC880C880u : 0xD480D480u;
+    r[0] = fma2((w & 0x000F000Fu) | 0x64006400u, m0, c0);
+    r[1] = fma2((w & 0x00F000F0u) | 0x64006400u, m1, c1);
     w >>= 8;
-    r[2] = fma2((w & 0x000F000Fu) | 0x64006400u, 0x30003000u, 0xD808D808u);
-    r[3] = fma2((w & 0x00F000F0u) | 0x64006400u, 0x20002000u, 0xC880C880u);
+    r[2] = fma2((w & 0x000F000Fu) | 0x64006400u, m0, c0);
+    r[3] = fma2((w & 0x00F000F0u) | 0x64006400u, m1, c1);
   } else {
     kv::e2m1_pairs(w, r);
   }
   return make_uint4(mul2(r[0], s), mul2(r[1], s), mul2(r[2], s), mul2(r[3], s));
 }
+
+// What the softmax has to know of 32 tokens, a bit each (uint4): .x the page is missing, .y a scale of V is no finite
+// number (stored as zero), .z the row of K, .w that of V holds an eighth.
 
 struct Params {
   AttendArgs a;
@@ -202,8 +212,9 @@ struct Lay {
   static constexpr int TB = CH * 128 * 128;               // bytes of a K or V tile [CH][128 tokens][128 bytes]
   static constexpr int K_OFF = GROUPS * TB;               // two of them
   static constexpr int V_OFF = K_OFF + 2 * TB;
-  static constexpr int MASK_OFF = V_OFF + 2 * TB;         // [4 tiles][4 warps] (page missing, V scale not finite)
-  static constexpr int BAR_OFF = MASK_OFF + 4 * 4 * 8;
+  static constexpr int MASK_OFF = V_OFF + 2 * TB;         // [4 tiles][4 warps] uint4 of marks
+  static constexpr int SUM_OFF = MASK_OFF + 4 * 4 * 16;   // [4 tiles][4 warps] bit 0: .x or .y, 1: .z, 2: .w has a mark
+  static constexpr int BAR_OFF = SUM_OFF + 4 * 4 * 4;
   static constexpr int NBAR = 8 + 3 * GROUPS + 3;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int TOTAL = MISC_OFF + 16 + 1024;
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       int e2 = 12 + 127 - (int)(__float_as_uint(amax) >> 23);
       e2 = amax == 0.0f || amax == INFINITY ? 0 : min(e2, 112);
       const float up = copysignf(__uint_as_float((uint32_t)(127 + e2) << 23), a.scale);
-      const float kg = FMT == WQ_NVFP4 ? (a.kv.g[0] ? *a.kv.g[0] : 1.0f) : 8.0f;
+      const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f;
       fac = fabsf(a.scale) * kLog2e * kg * __uint_as_float((uint32_t)(127 - e2) << 23);
       uint8_t* row = smem + L::Q_OFF + grp * L::TB + (threadIdx.x & 127) * 128;
 #pragma unroll 4
@@ -336,20 +347,29 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         if (!wait_all(&sfull[grp], j & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const int t0 = (tile0 + j) * kTile;
-        const uint2* flags = reinterpret_cast<const uint2*>(smem + L::MASK_OFF) + (j & 3) * 4;
-        uint32_t odd = 0;
+        const uint4* marks = reinterpret_cast<const uint4*>(smem + L::MASK_OFF) + (j & 3) * 4;
+        const uint4 sum = *reinterpret_cast<const uint4*>(smem + L::SUM_OFF + (j & 3) * 16);
+        const uint32_t odd = sum.x | sum.y | sum.z | sum.w;
+        if (FMT == WQ_Q4_0 && (odd & 2u)) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(s_at + c, v);
+            wait_ld(v);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint2 f = flags[w];
-          odd |= f.x | f.y;
+            for (int k = 0; k < 32; ++k)
+              if ((marks[c >> 5].z >> k) & 1u) v[k] = __float_as_uint(__uint_as_float(v[k]) * 8.0f);
+            tmem_st32(s_at + c, v);
+          }
+          tc_wait_st();
         }
-        const bool masked = __any_sync(0xFFFFFFFFu, t0 < lo || t0 + kTile > hi || odd != 0);
+        const bool masked = __any_sync(0xFFFFFFFFu, t0 < lo || t0 + kTile > hi || (odd & 1u));
         // what this row sees of the 32 tokens from c on, as bits
         auto sees = [&](int c) -> uint32_t {
           const int first = lo - (t0 + c), past = hi - (t0 + c);
           uint32_t bits = past >= 32 ? 0xFFFFFFFFu : past <= 0 ? 0u : (1u << past) - 1u;
           if (first > 0) bits = first >= 32 ? 0u : bits & ~((1u << first) - 1u);
-          return bits & ~flags[c >> 5].x;
+          return bits & ~marks[c >> 5].x;
         };
         // Loops are kept short (the roles share the instruction caches) and chains apart (four maxima, four sums).
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -374,6 +394,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         }
         float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top == -INFINITY ? top : top * fac;
+        if (FMT == WQ_Q4_0 && (odd & 4u)) top += 3.0f;   // a weight taken eightfold has to fit too
         const bool move = top > m + kSlack || (m == -INFINITY && top > m);
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float f = move ? ex2(m - top) : 1.0f;
@@ -411,7 +432,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
           }
           if (masked) {                 // not by the score alone: -inf times a scale of zero is no number
             const uint32_t see = sees(c);
-            if (see & flags[c >> 5].y) l = __uint_as_float(0x7FC00000u);   // a value that is no number
+            if (see & marks[c >> 5].y) l = __uint_as_float(0x7FC00000u);   // a value that is no number
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : 0u;
           }
@@ -427,6 +448,21 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         split(add2f(sums[0], sums[1]), even, odd_sum);
         l += even + odd_sum;
         tc_wait_st();
+        if (FMT == WQ_Q4_0 && (odd & 4u)) {      // a column of P holds two tokens
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(s_at + c, v);
+            wait_ld(v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t bits = marks[(c >> 4) + (k >> 4)].w >> (2 * (k & 15));
+              v[k] = mul2(v[k], 0x3C003C00u + (bits & 1u) * 0x0C00u + (bits & 2u) * 0x06000000u);
+            }
+            tmem_st32(s_at + c, v);
+          }
+          tc_wait_st();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[grp]);
@@ -436,7 +472,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     }
     // O / l to the output, or O, m and l as they are to this part's place
     const bool some = mine && tiles > 0 && l != 0.0f;
-    const float vg = FMT == WQ_NVFP4 ? (a.kv.g[1] ? *a.kv.g[1] : 1.0f) : 8.0f;
+    const float vg = FMT == WQ_NVFP4 && a.kv.g[1] ? *a.kv.g[1] : 1.0f;
     const float mul = p.parts > 1 ? vg : some ? vg / l : 0.0f;
     const bool row_there = ok && i < a.tokens;
     const int64_t at = p.parts > 1 ? ((b * a.kv.heads + h) * p.row_tiles + rt) * p.parts * (GROUPS * 128) +
@@ -512,7 +548,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       }
     };
     // A row of codes to its place in an operand tile.
-    auto store = [&](uint8_t* tile, const uint4 (&codes)[D / 32], const uint32_t (&scales)[SB / 4]) {
+    auto store = [&](uint8_t* tile, const uint4 (&codes)[D / 32], const uint32_t (&scales)[SB / 4], bool eighth) {
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
         const uint32_t w[4] = {codes[e].x, codes[e].y, codes[e].z, codes[e].w};
@@ -527,7 +563,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         for (int o = 0; o < 4; ++o) {
           const int oct = 4 * e + o;
           *reinterpret_cast<uint4*>(tile + (oct >> 3) * 16384 + r * 128 + (((oct & 7) ^ (r & 7)) << 4)) =
-              operand8<FMT>(w[o], o < 2 ? s0 : s1);
+              operand8<FMT>(w[o], o < 2 ? s0 : s1, eighth);
         }
       }
     };
@@ -550,15 +586,29 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
             bad = true;
           }
         }
-      const uint32_t missing = __ballot_sync(0xFFFFFFFFu, row == -2), bads = __ballot_sync(0xFFFFFFFFu, bad);
+      uint4 marks = make_uint4(__ballot_sync(0xFFFFFFFFu, row == -2), __ballot_sync(0xFFFFFFFFu, bad), 0u, 0u);
+      uint32_t kl = 0, vl = 0;
+      if (FMT == WQ_Q4_0) {
+#pragma unroll
+        for (int e = 0; e < SB / 4; ++e) {
+          kl |= large(raw.ks[e]);
+          vl |= large(raw.vs[e]);
+        }
+        marks.z = __ballot_sync(0xFFFFFFFFu, kl != 0);
+        marks.w = __ballot_sync(0xFFFFFFFFu, vl != 0);
+      }
       if (j >= 2 && !wait_all(&kempty[buf], ((j >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
-      if (lane == 0) reinterpret_cast<uint2*>(smem + L::MASK_OFF)[(j & 3) * 4 + dw] = make_uint2(missing, bads);
-      store(smem + L::K_OFF + buf * L::TB, raw.k, raw.ks);
+      if (lane == 0) {
+        reinterpret_cast<uint4*>(smem + L::MASK_OFF)[(j & 3) * 4 + dw] = marks;
+        reinterpret_cast<uint32_t*>(smem + L::SUM_OFF)[(j & 3) * 4 + dw] =
+            ((marks.x | marks.y) != 0 ? 1u : 0u) | (marks.z != 0 ? 2u : 0u) | (marks.w != 0 ? 4u : 0u);
+      }
+      store(smem + L::K_OFF + buf * L::TB, raw.k, raw.ks, kl != 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&kfull[buf]);
       if (j >= 2 && !wait_all(&vempty[buf], ((j >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
-      store(smem + L::V_OFF + buf * L::TB, raw.v, raw.vs);
+      store(smem + L::V_OFF + buf * L::TB, raw.v, raw.vs, vl != 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&vfull[buf]);

@@ -332,7 +332,9 @@ int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, i
  * max_len: what the caller knows on the host of lens (an upper bound, used to
  * plan the split of long sequences only; 0 stands for the capacity).
  * scale: finite.  Softmax statistics and sums are fp32; K, V and the weights enter
- * the products with 11 significant bits.
+ * the products with 11 significant bits, whatever the size of the scales (the weights
+ * down to 2^-25 of a row's largest, absolutely below; q4_0 values beside a block whose
+ * |d| is 8192 or more to 2^-22, with more than 32 query rows per cached head).
  * A NaN query, key or key scale makes the rows that see it NaN.  A V block whose scale
  * is not finite makes its own elements of the rows that see the token non-finite, or,
  * with more than 32 query rows per cached head (tokens * q_heads / heads), the
