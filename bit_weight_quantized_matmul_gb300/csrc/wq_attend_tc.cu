@@ -308,7 +308,8 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     float fac = 0.0f, m = -INFINITY, l = 0.0f;
     bool ok = true;
     if (tiles > 0 && grp < groups) {
-      // Q: the row times 2^e with its largest element in 2^12 .. 2^13 (and the sign of the scale), fp16
+      // Q: the row times 2^e with its largest element in 2^12 .. 2^13, fp16, and with the signs of the scale and of g: the
+      // largest score has to be the largest product
       const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token + hq * a.q.head;
       float amax = 0.0f;
 #pragma unroll 4
@@ -320,9 +321,9 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       }
       int e2 = 12 + 127 - (int)(__float_as_uint(amax) >> 23);
       e2 = amax == 0.0f || amax == INFINITY ? 0 : min(e2, 112);
-      const float up = copysignf(__uint_as_float((uint32_t)(127 + e2) << 23), a.scale);
       const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f;
-      fac = fabsf(a.scale) * kLog2e * kg * __uint_as_float((uint32_t)(127 - e2) << 23);
+      const float up = copysignf(__uint_as_float((uint32_t)(127 + e2) << 23), a.scale) * copysignf(1.0f, kg);
+      fac = fabsf(a.scale) * kLog2e * fabsf(kg) * __uint_as_float((uint32_t)(127 - e2) << 23);
       uint8_t* row = smem + L::Q_OFF + grp * L::TB + (threadIdx.x & 127) * 128;
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
