@@ -218,13 +218,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
 
   // The rows' tokens and what they see.
   const int n = kv::count_of(a.counts, b, a.tokens);
-  int len = max(a.lens[b], 0);
-  if (len > a.kv.capacity) {
-    if (threadIdx.x == 0) set_status(WQ_STATUS_ARG);
-    len = (int)a.kv.capacity;
-  }
+  const int len = max(a.lens[b], 0);                          // positions are counted from here
+  const int held = (int)min((int64_t)len, a.kv.capacity);     // what can be seen of them
+  if (held < len && threadIdx.x == 0) set_status(WQ_STATUS_ARG);
   const int64_t rows = (int64_t)n * p.group;                  // rows of this sequence
-  auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)len, (int64_t)len - n + i + 1)) : len; };
+  auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)held, (int64_t)len - n + i + 1)) : held; };
   auto lo_of = [&](int64_t i) { return a.window ? (int)max((int64_t)0, (int64_t)len - n + i - a.window + 1) : 0; };
   const int64_t i_first = r0 / p.group, i_last = min(rows - 1, r0 + 8 * NT - 1) / p.group;
   const bool any = r0 < rows;
@@ -244,8 +242,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   // rows would not fit the GPU), -1: past the end, -2: no such page.
   constexpr int kSpan = 32 / kGroups;
   auto locate = [&](int first) -> int {
-    const int tile = first + lane / kGroups * kWarps, t = tile * kTile + 16 * (lane % kGroups);
-    if (tile >= t_end || t >= hi_max) return -1;
+    const int tile = first + lane / kGroups * kWarps;
+    if (tile >= t_end) return -1;             // whose position may pass 32 bits
+    const int t = tile * kTile + 16 * (lane % kGroups);
+    if (t >= hi_max) return -1;
     int64_t page = b;
     int off = t;
     if (a.kv.table) {

@@ -281,13 +281,11 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
   const uint32_t tmem = *tmem_slot;
 
   const int n = kv::count_of(a.counts, b, a.tokens);
-  int len = max(a.lens[b], 0);
-  if (len > a.kv.capacity) {
-    if (threadIdx.x == 0) set_status(WQ_STATUS_ARG);
-    len = (int)a.kv.capacity;
-  }
+  const int len = max(a.lens[b], 0);                          // positions are counted from here
+  const int held = (int)min((int64_t)len, a.kv.capacity);     // what can be seen of them
+  if (held < len && threadIdx.x == 0) set_status(WQ_STATUS_ARG);
   const int64_t r0 = (int64_t)rt * GROUPS * 128, rows = (int64_t)n * p.group;
-  auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)len, (int64_t)len - n + i + 1)) : len; };
+  auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)held, (int64_t)len - n + i + 1)) : held; };
   auto lo_of = [&](int64_t i) { return a.window ? (int)max((int64_t)0, (int64_t)len - n + i - a.window + 1) : 0; };
   const bool any = r0 < rows;
   const int lo_min = any ? lo_of(r0 / p.group) : 0;
@@ -521,8 +519,9 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     };
     // Row of this thread's token in tile j; -1: past the end, -2: no such page.
     auto locate = [&](int j) -> int64_t {
+      if (j >= tiles) return -1;               // whose position may pass 32 bits
       const int t = (tile0 + j) * kTile + r;
-      if (j >= tiles || t >= hi_max) return -1;
+      if (t >= hi_max) return -1;
       int64_t page = b;
       int off = t;
       if (a.kv.table) {

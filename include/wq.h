@@ -321,7 +321,7 @@ int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, i
  * h / (q_heads / heads).  lens[b] is the number of tokens that sequence b holds
  * (those of this call included: append first).  counts as above: the last
  * counts[b] positions are this call's query tokens; query i sits at position
- * p = lens[b] - counts[b] + i.
+ * p = lens[b] - counts[b] + i (also where lens[b] is past the capacity).
  *   visible tokens   0 <= t < lens[b]; with WQ_FLAG_CAUSAL also t <= p, and with
  *                    window > 0 (WQ_FLAG_CAUSAL only) also t > p - window
  *   out              bf16, or fp32 with WQ_FLAG_OUT_F32, [batch, tokens, q_heads, dim]

@@ -18,3 +18,31 @@ def test_attend_with_negative_global_scales(signs, tokens, scale):
     case = Case(83, "nvfp4", 2, 128, 2, 400, 16)
     case.g = tuple(np.float32(s * g) for s, g in zip(signs, case.g))
     check_attend(case, tokens, 4, [400, 211], scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "nvfp4"])
+@pytest.mark.parametrize("tokens", [4, 40])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("page", [0, 16])
+def test_attend_lengths_past_the_capacity(fmt, tokens, window, page):
+    """A length past the capacity is reported; the query rows keep their positions at its end, and see what there is."""
+    need_gpu()
+    m, case = wq(), Case(84, fmt, 2, 64, 3, 64, page)
+    lens = [70, 64, 2 ** 31 - 1]
+    q = bf16(case.rng, 3, tokens, 4, 64)
+    assert m.last_device_status() == 0
+    out, lse = m.attend(case.upload(), q.cuda(), ints(lens), window=window, out_f32=True, return_lse=True)
+    assert m.last_device_status() == m.WQ_ERR_ARG
+    for b in range(3):
+        k, v = case.values(b, 64)
+        p = lens[b] - tokens + np.arange(tokens)
+        for i in range(tokens):
+            lo = max(0, p[i] - window + 1) if window else 0
+            hi = min(64, p[i] + 1)
+            got, gl = out[b, i].cpu().double().numpy(), lse[b, i].cpu().double().numpy()
+            if hi <= lo:
+                assert not got.any() and np.isneginf(gl).all()
+                continue
+            ref, rlse, mean, top = OK.attend(q[b, i:i + 1].float().numpy(), k[lo:hi], v[lo:hi], 1, 0.125, False)
+            assert np.all(np.abs(got - ref[0]) <= (2.0 ** -11 * (2 * top[0][:, None] + 4) + 2.0 ** -20) * mean[0] + 1e-30)
+            assert np.all(np.abs(gl - rlse[0]) <= 2.0 ** -11 * top[0] + 2.0 ** -20 * np.abs(rlse[0]) + 2.0 ** -20)
