@@ -449,7 +449,7 @@ int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, 
   a.counts = counts;
   a.max_len = max_len;
   a.scale = scale;
-  a.window = window;
+  a.window = window < (int64_t(1) << 31) ? window : int64_t(1) << 31;  // no wider: positions are below 2^31, and nothing overflows
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
   return attend(a, reinterpret_cast<cudaStream_t>(stream));

@@ -46,3 +46,30 @@ def test_attend_lengths_past_the_capacity(fmt, tokens, window, page):
             ref, rlse, mean, top = OK.attend(q[b, i:i + 1].float().numpy(), k[lo:hi], v[lo:hi], 1, 0.125, False)
             assert np.all(np.abs(got - ref[0]) <= (2.0 ** -11 * (2 * top[0][:, None] + 4) + 2.0 ** -20) * mean[0] + 1e-30)
             assert np.all(np.abs(gl - rlse[0]) <= 2.0 ** -11 * top[0] + 2.0 ** -20 * np.abs(rlse[0]) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("window", [20000, 2 ** 31, 2 ** 63 - 1])
+def test_attend_with_a_window_wider_than_all(tokens, window):
+    """Is planned and computed as no window: equal bits, and as many launches."""
+    need_gpu()
+    m, case = wq(), Case(85, "q4_0", 1, 64, 1, 20000, 64)
+    cache, q, lens = case.upload(), bf16(case.rng, 1, tokens, 2, 64).cuda(), ints([20000])
+    before = m.lib.wq_kernel_launches()
+    want = m.attend(cache, q, lens)
+    launches = m.lib.wq_kernel_launches() - before
+    got = m.attend(cache, q, lens, window=window)
+    assert torch.equal(got, want) and m.lib.wq_kernel_launches() - before == 2 * launches
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 40])
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 63 - 40, 2 ** 63 - 1])
+@pytest.mark.parametrize("page", [0, 16])
+def test_the_widest_windows_of_rows_before_the_first_token(tokens, window, page):
+    """p - window is below every 64-bit number for some of these rows: they see nothing, the others all there is."""
+    need_gpu()
+    m, case = wq(), Case(86, "q4_0", 2, 64, 5, 48, page)
+    cache, q, lens = case.upload(), bf16(case.rng, 5, tokens, 4, 64).cuda(), ints([0, 1, 2, 17, 45])
+    want, wlse = m.attend(cache, q, lens, return_lse=True)
+    got, lse = m.attend(cache, q, lens, window=window, return_lse=True)
+    assert torch.equal(got, want) and torch.equal(lse, wlse) and m.last_device_status() == 0
