@@ -263,16 +263,16 @@ class KVCache:
         for t in (k_codes, v_codes):
             assert t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous() and t.shape == k_codes.shape
         for t in (k_scales, v_scales):
-            assert t.is_cuda and t.dtype == stype and t.is_contiguous() and tuple(t.shape) == sshape
+            assert t.dtype == stype and t.is_contiguous() and tuple(t.shape) == sshape
         for t in (k_g, v_g):
-            assert t is None or (t.is_cuda and t.dtype == torch.float32 and t.numel() == 1)
-        assert table is None or (table.is_cuda and table.dtype == torch.int32 and table.dim() == 2
-                                 and table.is_contiguous())
+            assert t is None or (t.dtype == torch.float32 and t.numel() == 1)
+        assert table is None or (table.dtype == torch.int32 and table.dim() == 2 and table.is_contiguous())
         self.fmt, self.pages, self.heads, self.page_size, self.dim = f, pages, heads, page_size, dim
         self.capacity = page_size if table is None else table.shape[1] * page_size
         self.batch = pages if table is None else table.shape[0]
         self.tensors = (k_codes, k_scales, v_codes, v_scales, table, k_g, v_g)
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
+        assert all(t is None or t.get_device() == self.index for t in self.tensors)
         opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self.c = wq_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                              opt(k_g), opt(v_g), opt(table), 0 if table is None else table.shape[1], pages, page_size,
@@ -295,27 +295,37 @@ _kv_append, _kv_read = lib.wq_kv_append, lib.wq_kv_read
 _attend, _attend_workspace = lib.wq_attend, lib.wq_attend_workspace_bytes
 
 
-def _heads(t, dtype):
+def _heads(cache, t, dtype):
     """[batch, token, head, dim] view -> the bytes of a wq_heads (dim contiguous; other strides as they are)."""
     sb, st, sh, sd = t.stride()
-    assert t.is_cuda and t.dtype is dtype and sd == 1
+    assert t.get_device() == cache.index and t.dtype is dtype and sd == 1
     return _pack_heads(t.data_ptr(), sb, st, sh)
 
 
-def _index(t, batch):
+def _index(cache, t, batch):
     if t is None:
         return None
-    assert t.is_cuda and t.dtype is torch.int32 and t.is_contiguous() and t.numel() == batch
+    assert t.get_device() == cache.index and t.dtype is torch.int32 and t.is_contiguous() and t.numel() == batch
     return t.data_ptr()
+
+
+def _cache_stream(cache):
+    """The current stream of the cache's device, which has to be the current one."""
+    index = torch._C._cuda_getDevice()
+    assert index == cache.index, f"the cache is on device {cache.index}, the current device is {index}"
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def kv_append(cache, k, v, start=None, counts=None, stream=None):
     """Quantise k, v (bf16 [batch, tokens, heads, dim] views) into positions start[b] .. start[b] + counts[b] - 1
     of the cache (int32 CUDA tensors; None: 0, and all tokens)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_append(cache, k, v, start, counts)
     batch, tokens, heads, dim = k.shape
     assert v.shape == k.shape and heads == cache.heads and dim == cache.dim and batch <= cache.batch
-    rc = _kv_append(cache.ref, _heads(k, torch.bfloat16), _heads(v, torch.bfloat16), batch, tokens,
-                    _index(start, batch), _index(counts, batch), _stream(stream))
+    rc = _kv_append(cache.ref, _heads(cache, k, torch.bfloat16), _heads(cache, v, torch.bfloat16), batch, tokens,
+                    _index(cache, start, batch), _index(cache, counts, batch), _cache_stream(cache))
     if rc:
         raise WQError("wq_kv_append", rc)
 
@@ -333,8 +343,8 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     dt = torch.float32 if out_f32 else torch.bfloat16
     k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
     v = torch.empty_like(k)
-    rc = _kv_read(cache.ref, _heads(k, dt), _heads(v, dt), batch, tokens, _index(start, batch), _index(counts, batch),
-                  WQ_FLAG_OUT_F32 if out_f32 else 0, _stream())
+    rc = _kv_read(cache.ref, _heads(cache, k, dt), _heads(cache, v, dt), batch, tokens, _index(cache, start, batch),
+                  _index(cache, counts, batch), WQ_FLAG_OUT_F32 if out_f32 else 0, _cache_stream(cache))
     if rc:
         raise WQError("wq_kv_read", rc)
     return k, v
@@ -369,11 +379,14 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
         need = _attend_workspace(cache.ref, batch, tokens, q_heads, max_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    rc = _attend(cache.ref, _heads(q, torch.bfloat16), _heads(out, dt), None if lse is None else lse.data_ptr(), batch,
-                 tokens, q_heads, _index(lens, batch), _index(counts, batch), max_len, dim ** -0.5 if scale is None else scale,
-                 window, (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
+    else:
+        assert workspace.get_device() == cache.index and workspace.dtype is torch.uint8 and workspace.is_contiguous()
+    rc = _attend(cache.ref, _heads(cache, q, torch.bfloat16), _heads(cache, out, dt), None if lse is None else lse.data_ptr(), batch,
+                 tokens, q_heads, _index(cache, lens, batch), _index(cache, counts, batch), max_len,
+                 dim ** -0.5 if scale is None else scale, window,
+                 (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
                  None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-                 _stream())
+                 _cache_stream(cache))
     if rc:
         raise WQError("wq_attend", rc)
     return (out, lse) if return_lse else out

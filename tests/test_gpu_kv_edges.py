@@ -73,3 +73,41 @@ def test_the_widest_windows_of_rows_before_the_first_token(tokens, window, page)
     want, wlse = m.attend(cache, q, lens, return_lse=True)
     got, lse = m.attend(cache, q, lens, window=window, return_lse=True)
     assert torch.equal(got, want) and torch.equal(lse, wlse) and m.last_device_status() == 0
+
+
+def test_memory_that_is_not_the_caches_devices_is_refused(monkeypatch):
+    """Before any launch: host memory, another device's, a current device that is not the cache's."""
+    need_gpu()
+    m, case = wq(), Case(87, "q4_0", 2, 64, 2, 20000, 64)
+    cache, q, lens = case.upload(), bf16(case.rng, 2, 1, 4, 64).cuda(), ints([20000, 3])
+    k = bf16(case.rng, 2, 1, 2, 64).cuda()
+    need = m.attend_workspace_bytes(cache, 2, 1, 4)
+    assert need > 0
+    want = m.attend(cache, q, lens)
+    t, launches = cache.tensors, m.lib.wq_kernel_launches()
+    workspaces = [torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.float32, device="cuda"),
+                  torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]]
+    calls = [lambda w=w: m.attend(cache, q, lens, workspace=w) for w in workspaces]
+    calls += [lambda: m.attend(cache, q.cpu(), lens), lambda: m.attend(cache, q, lens.cpu()), lambda: m.attend(cache, q, lens, lens.cpu()),
+              lambda: m.attend(cache, q, lens, out=torch.empty_like(q, device="cpu")), lambda: m.kv_append(cache, k, k.cpu()),
+              lambda: m.kv_append(cache, k, k, lens.cpu()), lambda: m.kv_read(cache, 3, counts=lens.cpu()),
+              lambda: m.KVCache("q4_0", t[0], t[1], t[2].cpu(), t[3], t[4]), lambda: m.KVCache("q4_0", t[0], t[1].cpu(), t[2], t[3], t[4]),
+              lambda: m.KVCache("q4_0", *t[:4], t[4].cpu())]
+    for call in calls:
+        with pytest.raises(AssertionError):
+            call()
+    with pytest.raises(m.WQError):
+        m.attend(cache, q, lens, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    here = [lambda: m.attend(cache, q, lens), lambda: m.kv_append(cache, k, k), lambda: m.kv_read(cache, 3)]
+    with monkeypatch.context() as mp:
+        mp.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+        for call in here:
+            with pytest.raises(AssertionError):
+                call()
+    cache.index = 1
+    for call in here:
+        with pytest.raises(AssertionError):
+            call()
+    cache.index = 0
+    assert m.lib.wq_kernel_launches() == launches
+    assert torch.equal(m.attend(cache, q, lens, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")), want)
