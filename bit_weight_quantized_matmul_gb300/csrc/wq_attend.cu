@@ -1001,9 +1001,8 @@ int launch_join(const Params& p, int tile_rows, cudaStream_t s) {
 
 template <int FMT, int D, int NT>
 int launch(const Params& p, cudaStream_t s) {
-  static cudaError_t attr = cudaFuncSetAttribute(attend_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 smem_bytes(D, NT));
-  if (attr != cudaSuccess) return WQ_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (!allow_smem(allowed, attend_kernel<FMT, D, NT>, smem_bytes(D, NT))) return WQ_ERR_CUDA;
   const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.cluster * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
   cudaLaunchConfig_t cfg{};

@@ -36,8 +36,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "wq_kv.cuh"
 
 namespace wq {
@@ -681,12 +679,8 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
 template <int FMT, int D, int GROUPS>
 int launch(const Params& p, cudaStream_t s) {
   using L = Lay<D, GROUPS>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(attend_tc_kernel<FMT, D, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
-  });
-  if (attr != cudaSuccess) return WQ_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (!allow_smem(allowed, attend_tc_kernel<FMT, D, GROUPS>, L::TOTAL)) return WQ_ERR_CUDA;
   const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
   attend_tc_kernel<FMT, D, GROUPS><<<(unsigned)grid, L::THREADS, L::TOTAL, s>>>(p);

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/wq.h"
+#include "wq_once.h"
 
 namespace wq {
 
@@ -35,6 +36,15 @@ inline size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 // Host-side launch counter (all translation units).
 void count_launch(int n = 1);
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device.  done: one per kernel, static.
+template <class Kernel>
+inline bool allow_smem(std::atomic<uint64_t>& done, Kernel* kern, int bytes) {
+  int device = -1;
+  return cudaGetDevice(&device) == cudaSuccess && once_per_device(done, device, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  });
+}
 
 // ---- pack / dequant / activation quantiser (wq_pack.cu)
 int pack_nf4(const float* W, int64_t N, int64_t K, uint8_t* packed, uint8_t* scales, cudaStream_t s);
