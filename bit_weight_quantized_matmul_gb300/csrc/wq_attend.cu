@@ -1,8 +1,8 @@
 // wq_attend.cu -- attention over the 4-bit KV cache, few query rows per cached head (decode).
 //
 // With x_t the codes of token t, S = scale * Q K^T and O = softmax(S) V are computed from the codes
-// as they lie in the cache.  A block owns one cached head of one sequence, up to 8 * NT query rows
-// (the query heads of the group times the tokens of the call) and a range of tokens; each of its
+// as they lie in the cache.  A block owns one cached head of one sequence, its up to 8 * NT query rows
+// (row r = token * group + head of the group) and a range of tokens; each of its
 // four warps streams 32-token tiles of that range through a ring of its own in shared memory
 // (cp.async: no wait of one warp on another) and keeps its own running maximum m, sum l and O,
 // joined at the end.  The transposed products put tokens (then head elements) on the 16-row side of
@@ -45,9 +45,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;   // tiles in a warp's ring
 constexpr int kSms = 152;
-// More query rows than this per cached head go to the tensor-memory kernel, whose tile holds 128: at 40 rows (8 x 4 heads
-// of 128 over 4096 tokens) it takes 31 us and this one 41, at 32 rows (8 x 8 heads over 4000) 61 and 39.
-constexpr int64_t kFewRows = 32;
+// More query rows than this per cached head go to the tensor-memory kernel, whose tile holds 128.  It takes the same time for
+// 8 rows as for 64; this one, with its rows in tiles of 32 past 32 for the comparison, by number of rows (8 sequences of 4096
+// tokens with 8 heads of 128, the join included):
+//   rows              8    16    24    32    40    64
+//   q4_0   this    17.4  22.4  42.9  43.6  65.4  66.2 us     the other  44.2  43.5  43.9  43.9  44.5  45.4
+//   NVFP4  this    18.4  22.4  34.1  34.8  51.8  52.3        the other  39.2  39.3  40.3  40.6  41.1  42.3
+constexpr int kFewRows = 32;
 // More registers a thread beat more warps: 4, 3 and 2 blocks of NT = 1 an SM read one sequence of 2^20 tokens at
 // 4.6, 5.6 and 5.3 TB/s.
 constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -68,11 +72,11 @@ constexpr int smem_bytes(int D, int NT) {
 struct Params {
   AttendArgs a;
   int group;        // query heads per cached head
-  int row_tiles;    // blocks of 8 * NT query rows per cached head
-  int cluster;      // blocks of a cluster, which share a range of the tokens of one row tile
-  int parts;        // clusters that share the tokens of one row tile
-  float* part_o;    // [row tile][part][8 * NT][D] unnormalised outputs
-  float* part_ml;   // [row tile][part][8 * NT][2] their m (base 2) and l
+  int cluster;      // blocks of a cluster, which share the tokens of a cached head (or 1)
+  int parts;        // or blocks that do, joined by the join kernel (or 1)
+  int row_tiles;    // join kernel: row tiles of a cached head
+  float* part_o;    // [row tile][part][row][D] unnormalised outputs
+  float* part_ml;   // [row tile][part][row][2] their m (base 2) and l
 };
 
 // Byte offset of 16-byte chunk `col` (a block of 32 codes) of token `row` in a tile: the chunks of
@@ -164,12 +168,7 @@ __device__ __forceinline__ constexpr int pair_lo(int p) { return FMT == WQ_Q4_0 
 template <int FMT>
 __device__ __forceinline__ constexpr int pair_hi(int p) { return FMT == WQ_Q4_0 ? p + 4 : 2 * p + 1; }
 
-// Write one output element.
-__device__ __forceinline__ void put(const AttendArgs& a, int64_t at, float v) {
-  if (a.f32) reinterpret_cast<float*>(a.out.p)[at] = v;
-  else reinterpret_cast<__nv_bfloat16*>(a.out.p)[at] = __float2bfloat16_rn(v);
-}
-
+// Write four output elements.
 __device__ __forceinline__ void put4(const AttendArgs& a, int64_t at, float4 v) {
   if (a.f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out.p) + at) = v;
   else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out.p) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
@@ -192,22 +191,19 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
 
   uint32_t x = blockIdx.x;
-  const int splits = p.cluster * p.parts;
+  const int splits = p.cluster * p.parts;   // one of them is 1
   const int split = x % splits;         // the blocks of a cluster are neighbours
   x /= splits;
-  const int64_t tile_id = x;            // (sequence, cached head, row tile)
-  const int rt = x % p.row_tiles;
-  x /= p.row_tiles;
+  const int64_t item = x;               // (sequence, cached head)
   const int h = x % a.kv.heads;
   const int64_t b = x / a.kv.heads;
 
   // Q is asked for first: its addresses need nothing that is still on its way.  Lane (g, q) holds row
   // 8 j + g's elements 32 blk + 8 q .. + 7 (rows past counts[b] too: they are there, and their columns unused).
-  const int64_t r0 = (int64_t)rt * 8 * NT;                    // first row: token r / group, head r % group
   uint4 qw[NT][NB];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const uint32_t r = (uint32_t)r0 + 8 * j + g, i = r / (uint32_t)p.group;
+    const uint32_t r = 8 * j + g, i = r / (uint32_t)p.group;
     const bool in = i < a.tokens;
     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token +
                           ((int64_t)h * p.group + (r - i * (uint32_t)p.group)) * a.q.head + 8 * q;
@@ -221,13 +217,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   const int len = max(a.lens[b], 0);                          // positions are counted from here
   const int held = (int)min((int64_t)len, a.kv.capacity);     // what can be seen of them
   if (held < len && threadIdx.x == 0) set_status(WQ_STATUS_ARG);
-  const int64_t rows = (int64_t)n * p.group;                  // rows of this sequence
+  const int rows = n * p.group;                               // rows of this sequence, 8 * NT at most
   auto hi_of = [&](int64_t i) { return a.causal ? (int)max((int64_t)0, min((int64_t)held, (int64_t)len - n + i + 1)) : held; };
   auto lo_of = [&](int64_t i) { return a.window ? (int)max((int64_t)0, (int64_t)len - n + i - a.window + 1) : 0; };
-  const int64_t i_first = r0 / p.group, i_last = min(rows - 1, r0 + 8 * NT - 1) / p.group;
-  const bool any = r0 < rows;
-  const int lo_min = any ? lo_of(i_first) : 0, hi_max = any ? hi_of(i_last) : 0;
-  const int lo_max = any ? lo_of(i_last) : 0, hi_min = any ? hi_of(i_first) : 0;
+  const int lo_min = n > 0 ? lo_of(0) : 0, hi_max = n > 0 ? hi_of(n - 1) : 0;
+  const int lo_max = n > 0 ? lo_of(n - 1) : 0, hi_min = n > 0 ? hi_of(0) : 0;
   const int tile0 = lo_min / kTile;
   const int ntiles = hi_max > lo_min ? (hi_max + kTile - 1) / kTile - tile0 : 0;
   const int per = (ntiles + splits - 1) / splits;
@@ -388,7 +382,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int64_t r = r0 + 8 * j + 2 * q + c, i = r / p.group;
+      const int r = 8 * j + 2 * q + c, i = r / p.group;
       c_lo[j][c] = r < rows ? lo_of(i) : 0;
       c_hi[j][c] = r < rows ? hi_of(i) : hi_max;
     }
@@ -710,7 +704,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
         float z = 0.0f;                 // 0 times O, all added up
 #pragma unroll
         for (int d = 0; d < 2 * NB; ++d) z = fmaf(o[j][d][c], 0.0f, fmaf(o[j][d][c + 2], 0.0f, z));
-        odd |= z != 0.0f && r0 + 8 * j + 2 * q + c < rows;
+        odd |= z != 0.0f && 8 * j + 2 * q + c < rows;
       }
     if (!__any_sync(0xFFFFFFFFu, odd)) break;
     reset();
@@ -783,7 +777,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   }
 
   // ---------------------------------------------------------------- joining the blocks of a cluster
-  // Each leaves its O, m and l in its own shared memory (warp 0's part), and takes every cluster'th
+  // Each leaves its O, m and l in its own shared memory (warp 0's part), and writes every cluster'th
   // vector of the joined rows.
   int first = 0, step = 1;
   if (p.cluster > 1) {
@@ -832,19 +826,17 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
     }
   }
 
-  const int64_t r = r0 + row, i = r / p.group;
+  const int i = row / p.group;
   if (!joins) {
   } else if (p.parts > 1) {
-    const int64_t slot = (tile_id * p.parts + split / p.cluster) * kRows + row;
-    if (part == 0 && first == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
+    const int64_t slot = (item * p.parts + split) * kRows + row;
+    if (part == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, sum);
 #pragma unroll
-    for (int k = 0; k < D / (4 * kPerRow); ++k) {
-      const int vec = part + k * kPerRow;
-      if (vec % step == first) *reinterpret_cast<float4*>(p.part_o + slot * D + 4 * vec) = acc[k];
-    }
+    for (int k = 0; k < D / (4 * kPerRow); ++k)
+      *reinterpret_cast<float4*>(p.part_o + slot * D + 4 * (part + k * kPerRow)) = acc[k];
   } else if (i < a.tokens) {
-    const int hq = h * p.group + (int)(r - i * p.group);
-    const bool some = r < rows && sum != 0.0f;
+    const int hq = h * p.group + row - i * p.group;
+    const bool some = row < rows && sum != 0.0f;
     const float inv = some ? 1.0f / sum : 0.0f;
     const int64_t at = b * a.out.batch + i * a.out.token + hq * a.out.head;
 #pragma unroll
@@ -932,7 +924,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 
 struct Plan {
   bool tc;           // the tensor-memory kernel
-  int nt, row_tiles, cluster, parts;
+  int nt;              // 8 rows each
+  int cluster, parts;  // blocks that share the tokens of a cached head, in a cluster or joined: one of the two is 1
   AttendTcPlan tcp;
   size_t slots;      // partial rows in the workspace
 };
@@ -946,8 +939,10 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   const int64_t seen = window > 0 && window + tokens < held ? window + tokens : held;
   pl.tc = rows > kFewRows;
   if (pl.tc) {
-    // two groups of rows a block where that leaves a block for every SM; tokens are shared where it does not,
-    // four tiles of 128 to a part at least
+    // Two groups of rows a block where that leaves a block for every SM, or where there is work for long (one group, two:
+    // 1024 tokens of 32/8 heads of 128 over 4096 137 and 84 us, 512 of 20/20 of 64 over 8192 68 and 60; below the bound
+    // 1024 of 16/16 of 128 over 1100 28 and 37, but 2 x 128 of 32/8 of 128 over 9000 88 and 63).  Tokens are shared where
+    // SMs are left, four tiles of 128 to a part at least.
     const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
     pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
     if (half == 1) pl.tcp.groups = 1;
@@ -962,8 +957,7 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     return pl;
   }
   pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  pl.row_tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
-  const int64_t blocks = batch * kv.heads * pl.row_tiles;
+  const int64_t blocks = batch * kv.heads;
   const int tile = tile_tokens(kv.dim, pl.nt);
   const int64_t tiles = (seen + tile - 1) / tile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
   int64_t want = (int64_t)kSms * blocks_per_sm(pl.nt) / (blocks > 0 ? blocks : 1);
@@ -1003,7 +997,7 @@ template <int FMT, int D, int NT>
 int launch(const Params& p, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   if (!allow_smem(allowed, attend_kernel<FMT, D, NT>, smem_bytes(D, NT))) return WQ_ERR_CUDA;
-  const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.cluster * p.parts;
+  const int64_t grid = p.a.batch * p.a.kv.heads * p.cluster * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -1040,7 +1034,7 @@ int attend(const AttendArgs& a, cudaStream_t s) {
   Params p{};
   p.a = a;
   p.group = (int)(a.q_heads / a.kv.heads);
-  p.row_tiles = pl.tc ? pl.tcp.row_tiles : pl.row_tiles;
+  p.row_tiles = pl.tc ? pl.tcp.row_tiles : 1;
   p.cluster = pl.cluster;
   p.parts = pl.parts;
   p.part_o = reinterpret_cast<float*>(a.workspace);
