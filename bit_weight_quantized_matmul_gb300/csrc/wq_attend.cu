@@ -27,12 +27,13 @@
 // with d / 8 and 8 p where d is large, and with such scales out of the product.
 //
 // Must read 0.5625 bytes an element of the visible K and V once.  Measured on GB300: one sequence of 2^20 tokens, 8 heads
-// of 128, 5.6 TB/s (q4_0) and 5.4 (NVFP4) of 6.8 for a copy; 57 x 8 heads x 4500 tokens (one block for every place on
-// the device) 62 us, 4.8 TB/s; 64 sequences of 1000 to 8000 89 us, 3.7 TB/s, for the blocks past the first 456 run
-// when most places are empty; one sequence of 131071 33 us and 5 for the join.  Bound by the instruction chain of a
-// warp: about 19 instructions per token and head of 128, 12 warps an SM for their registers, one issued every fourth
-// cycle or so, DRAM at 44 to 75 % of its peak.  Short sequences are bound by what a block does before its
-// first tile and after its last (about 4 us for each block that follows another in a place).
+// of 128, 226 us with the join, 5.3 TB/s of 6.8 for a copy (2^21 439 us, 5.5 TB/s); 57 x 8 heads x 4500 tokens (one
+// block for every place on the device) 65 us from a cold cache, 4.5 TB/s; 64 sequences of 1000 to 8000 89 us, 3.7 TB/s,
+// for the blocks past the first 456 run when most places are empty; one sequence of 131071 34 us and 5 for the join.
+// Bound by the instruction chain of a warp: 19 (NVFP4) to 21 (q4_0) instructions per token and head of 128, 12 warps
+// an SM for their registers, one issued every fourth cycle or so, DRAM at 45 to 75 % of its peak.  Short sequences are
+// bound by what a block does before its first tile and after its last (about 4 us for each block that follows another
+// in a place).  Heads of 128 with 17 to 32 rows do not fit the registers (q4_0 spills 588 bytes a thread, NVFP4 208).
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -24,12 +24,13 @@
 // A V scale that is no finite number cannot be left to the product (0 * NaN spoils rows that do not see
 // the token): the block is stored as zeros and the rows that do see the token are made NaN.
 //
-// Measured on GB300 (19 sequences of 16384 tokens, 8 cached heads of 128, 256 rows each, one block an SM): 1114
-// TFLOP/s (q4_0), 1177 (NVFP4), 0.58 and 0.61 of the measured bf16 rate.  Bound by a chain: a tile of 128 tokens
-// takes 4400 cycles, of which a row's softmax takes 2300 and its group's two products 1100, and the other group
-// has the tensor cores meanwhile.  Tried and slower: half tiles of 64 tokens with scores ahead of the
-// products (more, smaller MMAs: 815 TFLOP/s), one pass over S with P kept in registers (915), two threads a row (970),
-// a row's 128 scores in registers (spills), the codes of two tiles in registers (1118 / 1150).
+// Measured on GB300 (19 sequences of 16384 tokens, 8 cached heads of 128, 256 rows each, one block an SM): 1082
+// TFLOP/s (q4_0), 1169 (NVFP4), 0.56 and 0.61 of the measured bf16 rate.  Bound by a chain: a tile of 128 tokens
+// takes 4500 cycles, of which a row's softmax takes 2300 and its group's two products 1100, and the other group
+// has the tensor cores meanwhile.  Tried and slower, against 1114 (q4_0) before scales of 8192 and more were told
+// apart: half tiles of 64 tokens with scores ahead of the products (more, smaller MMAs: 815 TFLOP/s), one pass over S
+// with P kept in registers (915), two threads a row (970), a row's 128 scores in registers (spills), the codes of two
+// tiles in registers (1118 / 1150).
 //
 // Every wait is bounded; after one ran out the roles stop, and the MMAs issued are waited for before
 // tensor memory is released.
@@ -219,7 +220,8 @@ struct Lay {
   static constexpr int SOFT = 4 * GROUPS, DEC = SOFT, MMA = SOFT + 4;   // first warps of the roles
   static constexpr int THREADS = (SOFT + 5) * 32;
   static constexpr int COLS = GROUPS * (128 + D) <= 256 ? 256 : 512;    // tensor memory columns
-  // two blocks an SM where shared memory, tensor memory and registers hold them
+  // two blocks an SM where shared memory and tensor memory hold them: at 96 registers heads of 64 spill 36 to 52 bytes, and
+  // 4 x 224 tokens over 1500 of 20 heads take 38 us (q4_0), with one block an SM 53; 1 x 224, whose blocks all fit, 16 and 14
   static constexpr int BLOCKS = TOTAL <= 113 * 1024 && COLS <= 256 ? 2 : 1;
 };
 

@@ -3,7 +3,8 @@
 // Both move each element once (append: 2 bytes in, 9/16 out; read the other way round).  HBM bounds the reading (8 x
 // 12000 .. 16384 tokens of 8 heads of 128, NVFP4, to bf16: 103 us, 6.5 TB/s of 6.8 for a copy), instruction issue the
 // appending (16 x 1500 x 20 x 64, q4_0: 35 us, 4.5 TB/s; 132 instructions per eight elements, issued 85 % of the
-// time), the launch a call of few tokens.  A thread owns the same eight elements of a head in up to
+// time; 4 x 333 .. 2048 x 8 x 128, NVFP4: 10 us, at 8 blocks an SM, half of its warps there, issuing 65 % of the time
+// and waiting for the loads at the block's beginning), the launch a call of few tokens.  A thread owns the same eight elements of a head in up to
 // eight tokens of one sequence, whose loads are in flight together: one 16-byte access on the bf16 side,
 // four bytes of codes.  A q4_0 block is then four neighbouring lanes, an NVFP4 block two, and the
 // block's scale a maximum over them.
