@@ -43,6 +43,12 @@
 namespace wq {
 namespace {
 
+using kv::ex2;
+using kv::large;
+using kv::max3;
+using kv::mul2;
+using kv::pack_f16x2;
+
 constexpr int kWarps = 4;
 constexpr int kStages = 3;   // tiles in a warp's ring
 constexpr int kSms = 152;
@@ -124,16 +130,6 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Two fp32 operations in one instruction, each rounded as by itself.
 __device__ __forceinline__ void mul_pair(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
@@ -143,23 +139,11 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
       "add.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // The top bit of each scale in a word that is infinite or NaN.
 template <int FMT>
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
   return FMT == WQ_Q4_0 ? ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u : ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
-// The top bit of each half of an fp16 pair that is 8192 or more in magnitude (or no finite number).
-__device__ __forceinline__ uint32_t large(uint32_t x) { return ((x & 0x70007000u) + 0x10001000u) & 0x80008000u; }
 // For each half 1/8 (8) where it is large, else 1.
 __device__ __forceinline__ uint32_t eighth(uint32_t x) { return 0x3C003C00u - (large(x) >> 15) * 0x0C00u; }
 __device__ __forceinline__ uint32_t eightfold(uint32_t x) { return 0x3C003C00u + (large(x) >> 15) * 0x0C00u; }

@@ -42,6 +42,12 @@
 namespace wq {
 namespace {
 
+using kv::ex2;
+using kv::large;
+using kv::max3;
+using kv::mul2;
+using kv::pack_f16x2;
+
 constexpr int kTile = 128;      // tokens of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;  // how far (base 2) a score may pass m before m moves
@@ -124,21 +130,6 @@ __device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -161,13 +152,6 @@ __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// The top bit of each half of an fp16 pair that is 8192 or more, or no finite number.
-__device__ __forceinline__ uint32_t large(uint32_t x) { return ((x & 0x70007000u) + 0x10001000u) & 0x80008000u; }
 // Element of an octet that position e of an operand row holds.
 template <int FMT>
 __device__ __forceinline__ constexpr int octet(int e) { return FMT == WQ_Q4_0 ? (e & 1) * 4 + (e >> 1) : e; }

@@ -103,5 +103,29 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t b) {
   return r;
 }
 
+// ---- arithmetic of the attention kernels
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The top bit of each half of an fp16 pair that is 8192 or more in magnitude (or no finite number).
+__device__ __forceinline__ uint32_t large(uint32_t x) { return ((x & 0x70007000u) + 0x10001000u) & 0x80008000u; }
+
 }  // namespace kv
 }  // namespace wq
