@@ -190,8 +190,28 @@ int check_heads(const wq_heads* h, size_t esz, HeadsArg& a) {
   return WQ_OK;
 }
 
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
 bool too_many(int64_t batch, int64_t tokens) {
   return batch > 0x7FFFFFFF || tokens > 0x7FFFFFFF || batch * tokens > 0x7FFFFFFF;
+}
+
+// The part of a reserve or release call that the two share.
+int check_turn(const wq_kv_cache* cache, const int32_t* free_pages, int64_t free_size, const int32_t* top, int32_t* top_out,
+               int64_t batch, const int32_t* lens, KvReserveArgs& a) {
+  const int rc = check_cache(cache, a.kv);
+  if (rc != WQ_OK) return rc;
+  if (!cache->table || !top || !top_out || free_size < 0 || (free_size > 0 && !free_pages) || batch < 0 || (batch > 0 && !lens))
+    return WQ_ERR_ARG;
+  if (batch > WQ_TURN_MAX || free_size > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  if (!aligned(free_pages, 4) || !aligned(top, 4) || !aligned(top_out, 4) || !aligned(lens, 4)) return WQ_ERR_ALIGN;
+  a.free_pages = free_pages;
+  a.free_size = free_size;
+  a.top = top;
+  a.top_out = top_out;
+  a.batch = batch;
+  a.lens = lens;
+  return WQ_OK;
 }
 
 // The part of an append or read call that the two share; *rows: whether there is anything to do.
@@ -413,6 +433,79 @@ int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, i
   return kv_read(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int wq_kv_append_slots(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t tokens, const int64_t* slots,
+                       void* stream) {
+  KvSlotArgs a{};
+  int rc = check_cache(cache, a.kv);
+  if (rc != WQ_OK) return rc;
+  if (tokens < 0) return WQ_ERR_ARG;
+  if (tokens > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  if (tokens == 0) return WQ_OK;
+  if (!slots) return WQ_ERR_ARG;
+  if (!aligned(slots, 8)) return WQ_ERR_ALIGN;
+  if ((rc = check_heads(k, 2, a.x[0])) != WQ_OK || (rc = check_heads(v, 2, a.x[1])) != WQ_OK) return rc;
+  a.tokens = tokens;
+  a.slots = slots;
+  return kv_append_slots(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wq_kv_reserve(const wq_kv_cache* cache, const int32_t* free_pages, int64_t free_size, const int32_t* top, int32_t* top_out,
+                  int64_t batch, const int32_t* lens, const int32_t* counts, int32_t* granted, int64_t tokens, int64_t* slots,
+                  int32_t* positions, int32_t* starts, void* stream) {
+  KvReserveArgs a{};
+  const int rc = check_turn(cache, free_pages, free_size, top, top_out, batch, lens, a);
+  if (rc != WQ_OK) return rc;
+  if (tokens < 0 || (batch > 0 && !counts) || (granted && granted == counts)) return WQ_ERR_ARG;
+  if (tokens > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  if (!aligned(counts, 4) || !aligned(granted, 4) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(starts, 4))
+    return WQ_ERR_ALIGN;
+  a.counts = counts;
+  a.granted = granted;
+  a.tokens = slots || positions ? tokens : 0;
+  a.slots = slots;
+  a.positions = positions;
+  a.starts = starts;
+  return kv_reserve(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wq_kv_release(const wq_kv_cache* cache, int32_t* free_pages, int64_t free_size, const int32_t* top, int32_t* top_out,
+                  int64_t batch, const int32_t* lens, const int32_t* keep, void* stream) {
+  KvReserveArgs a{};
+  const int rc = check_turn(cache, free_pages, free_size, top, top_out, batch, lens, a);
+  if (rc != WQ_OK) return rc;
+  if (!aligned(keep, 4)) return WQ_ERR_ALIGN;
+  a.counts = keep;
+  return kv_release(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wq_kv_keep(const wq_kv_cache* cache, const int32_t* start, int64_t batch, const int32_t* path, int64_t path_ld,
+               const int32_t* counts, void* stream) {
+  KvKeepArgs a{};
+  const int rc = check_cache(cache, a.kv);
+  if (rc != WQ_OK) return rc;
+  if (batch < 0 || path_ld < 0) return WQ_ERR_ARG;
+  if (path_ld > WQ_PATH_MAX || batch > 0x7FFFFFFF || (!cache->table && batch > cache->pages)) return WQ_ERR_SHAPE;
+  if (batch == 0 || path_ld == 0) return WQ_OK;
+  if (!start || !path) return WQ_ERR_ARG;
+  if (!aligned(start, 4) || !aligned(path, 4) || !aligned(counts, 4)) return WQ_ERR_ALIGN;
+  a.batch = batch;
+  a.start = start;
+  a.path = path;
+  a.path_ld = path_ld;
+  a.counts = counts;
+  return kv_keep(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wq_tree_mask(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window, uint32_t* mask,
+                 int32_t* depth, void* stream) {
+  if (batch < 0 || tokens < 0 || window < 0) return WQ_ERR_ARG;
+  if (tokens > WQ_TREE_MAX || too_many(batch, tokens)) return WQ_ERR_SHAPE;
+  if (batch == 0 || tokens == 0) return WQ_OK;
+  if (!parents || !mask) return WQ_ERR_ARG;
+  if (!aligned(parents, 4) || !aligned(counts, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return WQ_ERR_ALIGN;
+  return tree_mask(parents, counts, batch, tokens, window, mask, depth, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
                                  int64_t max_len) {
   KvArgs kv{};
@@ -425,6 +518,14 @@ size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_
 int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
               int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
               float scale, int64_t window, unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+  return wq_attend_ex(cache, q, out, lse, batch, tokens, q_heads, lens, counts, max_len, scale, window, 0, nullptr, flags,
+                      workspace, workspace_bytes, stream);
+}
+
+int wq_attend_ex(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
+                 int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
+                 float scale, int64_t window, int64_t sinks, const wq_tree* tree, unsigned flags, void* workspace,
+                 size_t workspace_bytes, void* stream) {
   if (flags & ~(unsigned)(WQ_FLAG_OUT_F32 | WQ_FLAG_CAUSAL)) return WQ_ERR_ARG;
   AttendArgs a{};
   int rc = check_cache(cache, a.kv);
@@ -433,6 +534,18 @@ int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, 
   a.f32 = (flags & WQ_FLAG_OUT_F32) != 0;
   if (batch < 0 || tokens < 0 || q_heads < 0 || max_len < 0 || window < 0 || (window > 0 && !a.causal)) return WQ_ERR_ARG;
   if (!(scale > -INFINITY && scale < INFINITY)) return WQ_ERR_ARG;
+  if (sinks < 0 || (sinks > 0 && !a.causal)) return WQ_ERR_ARG;
+  if (tree) {
+    if (!a.causal || !tree->mask || tree->mask_batch < 0 || tree->depth_batch < 0) return WQ_ERR_ARG;
+    if (tokens > WQ_TREE_MAX) return WQ_ERR_SHAPE;
+    if (!aligned(tree->mask, 4) || !aligned(tree->depth, 4)) return WQ_ERR_ALIGN;
+    a.tree_mask = tree->mask;
+    a.tree_depth = tree->depth;
+    a.mask_batch = tree->mask_batch;
+    a.depth_batch = tree->depth_batch;
+    a.tree_words = (int32_t)((tokens + 31) / 32);
+  }
+  a.sinks = (int32_t)(sinks < 0x7FFFFFFF ? sinks : 0x7FFFFFFF);
   if (too_many(batch, tokens) || (!cache->table && batch > cache->pages) || q_heads > 65535 || q_heads % a.kv.heads != 0) return WQ_ERR_SHAPE;
   if (batch == 0 || tokens == 0 || q_heads == 0) return WQ_OK;
   if (!lens) return WQ_ERR_ARG;
@@ -471,9 +584,10 @@ int wq_selftest_encoders(const float* in, int64_t n, uint8_t* out, void* stream)
 int wq_last_device_status(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
   int worst = WQ_OK;
-  const int parts[9] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
+  const int parts[12] = {take_status_pack(), take_status_simt(), take_status_tc(), take_status_tcp(),
                         take_status_w4a4(), take_status_w4a16(), take_status_kv(), take_status_attend(),
-                        take_status_attend_tc()};
+                        take_status_attend_tc(), take_status_attend_few_sel(), take_status_attend_tc_sel(),
+                        take_status_pages()};
   for (int v : parts)
     if (v != WQ_OK) worst = v;
   return worst;

@@ -143,7 +143,46 @@ struct KvMoveArgs {
 };
 int kv_append(const KvMoveArgs& a, cudaStream_t s);
 int kv_read(const KvMoveArgs& a, cudaStream_t s);
+// Tokens laid end to end (x[..].batch unused), each to its slot.
+struct KvSlotArgs {
+  KvArgs kv;
+  HeadsArg x[2];
+  int64_t tokens;
+  const int64_t* slots;
+};
+int kv_append_slots(const KvSlotArgs& a, cudaStream_t s);
 int take_status_kv();
+
+// ---- pages, slots and trees (wq_pages.cu)
+struct KvReserveArgs {
+  KvArgs kv;
+  const int32_t* free_pages;   // release writes it
+  int64_t free_size;
+  const int32_t* top;
+  int32_t* top_out;            // may be top
+  int64_t batch;
+  const int32_t* lens;
+  const int32_t* counts;       // reserve: new tokens; release: tokens that stay (NULL: none)
+  int32_t* granted;
+  int64_t tokens;              // of the slot map
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* starts;
+};
+struct KvKeepArgs {
+  KvArgs kv;
+  int64_t batch;
+  const int32_t* start;
+  const int32_t* path;         // [batch, path_ld]
+  int64_t path_ld;
+  const int32_t* counts;
+};
+int kv_reserve(const KvReserveArgs& a, cudaStream_t s);
+int kv_release(const KvReserveArgs& a, cudaStream_t s);
+int kv_keep(const KvKeepArgs& a, cudaStream_t s);
+int tree_mask(const int32_t* parents, const int32_t* counts, int64_t batch, int64_t tokens, int64_t window, uint32_t* mask,
+              int32_t* depth, cudaStream_t s);
+int take_status_pages();
 
 struct AttendArgs {
   KvArgs kv;
@@ -158,18 +197,34 @@ struct AttendArgs {
   bool causal, f32;
   void* workspace;
   size_t workspace_bytes;
+  // Rows that see more than one run of tokens (the SEL kernels): the first `sinks` behind a window, drafted nodes by bits.
+  int32_t sinks;
+  int32_t tree_words;           // of a node's bits
+  const uint32_t* tree_mask;    // NULL: no tree
+  const int32_t* tree_depth;    // NULL: node i is at depth i
+  int64_t mask_batch, depth_batch;
 };
 size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len);
 int attend(const AttendArgs& a, cudaStream_t s);
 int take_status_attend();
-// Many query rows per cached head (wq_attend_tc.cu): groups of 128 rows a block, blocks that share the
-// tokens of a row tile (parts > 1: partial rows to the workspace, joined afterwards).
+// Few query rows per cached head (wq_attend_few.cuh; 8 * nt of them): blocks of a cluster, or parts joined afterwards, share
+// the tokens.  Many (wq_attend_tc.cuh): groups of 128 rows a block, parts that share the tokens of a row tile.  The _sel forms,
+// in translation units of their own, are for sinks and trees.
+struct AttendFewPlan {
+  int nt, cluster, parts;
+  size_t slots;
+};
 struct AttendTcPlan {
   int groups, row_tiles, parts;
   size_t slots;
 };
+int attend_few(const AttendArgs& a, const AttendFewPlan& pl, cudaStream_t s);
+int attend_few_sel(const AttendArgs& a, const AttendFewPlan& pl, cudaStream_t s);
 int attend_tc(const AttendArgs& a, const AttendTcPlan& pl, cudaStream_t s);
+int attend_tc_sel(const AttendArgs& a, const AttendTcPlan& pl, cudaStream_t s);
 int take_status_attend_tc();
+int take_status_attend_few_sel();
+int take_status_attend_tc_sel();
 
 // driver entry point for tensor-map encoding (resolved once through the runtime)
 bool encode_tmap_2d(void* tmap, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,

@@ -284,6 +284,41 @@ __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel
   }
 }
 
+// Tokens laid end to end, each to its slot: a thread owns the same eight elements of up to four neighbouring heads of a
+// token, so that one look-up serves them all and neighbouring bf16 is read together.
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_slots_kernel(const __grid_constant__ KvSlotArgs a, const int wide) {
+  constexpr int kPer = D / 8;
+  const int which = blockIdx.y, rounds = (a.kv.heads + kAppendRounds - 1) / kAppendRounds;
+  const int chunk = blockIdx.x / (unsigned)rounds, h0 = (blockIdx.x - chunk * rounds) * kAppendRounds;
+  const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8, heads = min(kAppendRounds, a.kv.heads - h0);
+  const int64_t i = (int64_t)chunk * wide + tok;
+  const bool in = tok < wide && i < a.tokens;
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(a.x[which].p) + i * a.x[which].token + h0 * a.x[which].head + e;
+  uint4 u[kAppendRounds];
+#pragma unroll
+  for (int k = 0; k < kAppendRounds; ++k)
+    u[k] = in && k < heads ? *reinterpret_cast<const uint4*>(src + k * a.x[which].head) : make_uint4(0, 0, 0, 0);
+  const float g = FMT == WQ_NVFP4 && a.kv.g[which] ? *a.kv.g[which] : 1.0f;
+  const int64_t slot = in ? a.slots[i] : -1;
+  int64_t row = -1;
+  if (slot >= 0) {
+    const int64_t page = slot >> 31 ? slot / a.kv.page_size : kv::page_of(a.kv, (int)slot);
+    if (page < a.kv.pages) row = (page * a.kv.heads + h0) * (int64_t)a.kv.page_size + (slot - page * a.kv.page_size);
+    else set_status(WQ_STATUS_ARG);
+  }
+#pragma unroll
+  for (int k = 0; k < kAppendRounds; ++k) {
+    if (k >= heads) break;             // for the whole block: its lanes exchange values
+    uint32_t sc;
+    const uint32_t w = encode8<FMT>(u[k], g, sc);
+    if (row < 0) continue;
+    const Place<D> p(a.kv, which, row + (int64_t)k * a.kv.page_size, e);
+    *reinterpret_cast<uint32_t*>(p.codes) = w;
+    store_scale<FMT>(p.scales, e, sc);
+  }
+}
+
 template <int FMT, bool F32>
 __device__ __forceinline__ void put8(void* p, int64_t at, uint32_t w, uint32_t sc, float g) {
   float v[8];
@@ -382,6 +417,15 @@ int append_t(const KvMoveArgs& a, cudaStream_t s) {
   kv_append_kernel<FMT, D><<<g.blocks, g.threads, 0, s>>>(a, g.wide);
   return launched();
 }
+template <int FMT, int D>
+int append_slots_t(const KvSlotArgs& a, cudaStream_t s) {
+  constexpr int kPer = D / 8;
+  const int wide = (int)(a.tokens < kThreads / kPer ? a.tokens : kThreads / kPer);
+  const int64_t blocks = (a.tokens + wide - 1) / wide * ((a.kv.heads + kAppendRounds - 1) / kAppendRounds);
+  if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  kv_append_slots_kernel<FMT, D><<<dim3((unsigned)blocks, 2), (wide * kPer + 31) / 32 * 32, 0, s>>>(a, wide);
+  return launched();
+}
 template <int FMT, int D, int ROUNDS>
 int read_t(const KvMoveArgs& a, const Grid& g, cudaStream_t s) {
   if (!g.ok) return WQ_ERR_SHAPE;
@@ -405,6 +449,11 @@ int read_t(const KvMoveArgs& a, cudaStream_t s) {
 int kv_append(const KvMoveArgs& a, cudaStream_t s) {
   if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? append_t<WQ_Q4_0, 64>(a, s) : append_t<WQ_Q4_0, 128>(a, s);
   return a.kv.dim == 64 ? append_t<WQ_NVFP4, 64>(a, s) : append_t<WQ_NVFP4, 128>(a, s);
+}
+
+int kv_append_slots(const KvSlotArgs& a, cudaStream_t s) {
+  if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? append_slots_t<WQ_Q4_0, 64>(a, s) : append_slots_t<WQ_Q4_0, 128>(a, s);
+  return a.kv.dim == 64 ? append_slots_t<WQ_NVFP4, 64>(a, s) : append_slots_t<WQ_NVFP4, 128>(a, s);
 }
 
 int kv_read(const KvMoveArgs& a, cudaStream_t s) {

@@ -66,6 +66,13 @@ class wq_heads(ctypes.Structure):
                 ("head", ctypes.c_int64)]
 
 
+class wq_tree(ctypes.Structure):
+    _fields_ = [("mask", ctypes.c_void_p), ("depth", ctypes.c_void_p), ("mask_batch", ctypes.c_int64),
+                ("depth_batch", ctypes.c_int64)]
+
+
+WQ_TURN_MAX, WQ_TREE_MAX, WQ_PATH_MAX = 65536, 1024, 512
+
 _P, _I64, _I, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint
 _SIGS = {
     "wq_packed_bytes": (ctypes.c_size_t, [_I, _I64, _I64]),
@@ -88,6 +95,13 @@ _SIGS = {
     "wq_attend_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64, _I64, _I64]),
     "wq_attend": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I64, _U, _P,
                        ctypes.c_size_t, _P]),
+    "wq_attend_ex": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I64, _I64, _P, _U, _P,
+                          ctypes.c_size_t, _P]),
+    "wq_kv_append_slots": (_I, [_P, _P, _P, _I64, _P, _P]),
+    "wq_kv_reserve": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P]),
+    "wq_kv_release": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P]),
+    "wq_kv_keep": (_I, [_P, _P, _I64, _P, _I64, _P, _P]),
+    "wq_tree_mask": (_I, [_P, _I64, _I64, _P, _I64, _P, _P, _P]),
     "wq_last_device_status": (_I, []),
     "wq_status_string": (ctypes.c_char_p, [_I]),
     "wq_kernel_launches": (ctypes.c_uint64, []),
@@ -293,6 +307,9 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
 _pack_heads = struct.Struct("Pqqq").pack
 _kv_append, _kv_read = lib.wq_kv_append, lib.wq_kv_read
 _attend, _attend_workspace = lib.wq_attend, lib.wq_attend_workspace_bytes
+_pack_tree = struct.Struct("PPqq").pack
+_attend_ex, _kv_append_slots, _kv_keep, _tree_mask = lib.wq_attend_ex, lib.wq_kv_append_slots, lib.wq_kv_keep, lib.wq_tree_mask
+_kv_reserve, _kv_release = lib.wq_kv_reserve, lib.wq_kv_release
 
 
 def _heads(cache, t, dtype):
@@ -350,12 +367,132 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
     return k, v
 
 
+def kv_append_slots(cache, k, v, slots, stream=None):
+    """Quantise k, v (bf16 [tokens, heads, dim] views of tokens laid end to end) into the cache, token i to slots[i] (int64
+    CUDA tensor, page * page_size + offset, as kv_reserve gives them; negative: skipped)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_append_slots(cache, k, v, slots)
+    tokens, heads, dim = k.shape
+    assert v.shape == k.shape and heads == cache.heads and dim == cache.dim
+    assert slots.get_device() == cache.index and slots.dtype is torch.int64 and slots.is_contiguous() and slots.numel() == tokens
+    rc = _kv_append_slots(cache.ref, _rows(cache, k), _rows(cache, v), tokens, slots.data_ptr(), _cache_stream(cache))
+    if rc:
+        raise WQError("wq_kv_append_slots", rc)
+
+
+def kv_reserve(cache, free, top, lens, counts, tokens, top_out=None, out=None, stream=None):
+    """Pages for counts[b] tokens behind the lens[b] that sequence b holds, written to the cache's table, and their slots.
+
+    free: int32 CUDA tensor, a stack of page numbers that nobody holds, of which the first top[0] (int32 [1]) count; lens,
+    counts: int32 [batch].  tokens: the length of the slot map, an upper bound of the sum of counts.  Returns
+    (slots int64 [tokens], positions int32 [tokens], starts int32 [batch + 1], granted int32 [batch]): each token's place
+    and position, all tokens laid end to end (-1 and 0 behind the last); where a sequence's begin; and counts[b], or 0
+    where the pages did not last (slots -1).  out: these four, to write to.  top_out: where the number of pages left
+    goes (default: top)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_reserve(cache, free, top, lens, counts, tokens, top_out, out)
+    batch, dev = _turn(cache, free, top, top_out, lens), cache.device
+    if out is None:
+        out = (torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int32, device=dev),
+               torch.empty(batch + 1, dtype=torch.int32, device=dev), torch.empty(batch, dtype=torch.int32, device=dev))
+    slots, positions, starts, granted = out
+    assert slots.get_device() == cache.index and slots.dtype is torch.int64 and slots.is_contiguous() and slots.numel() == tokens
+    rc = _kv_reserve(cache.ref, free.data_ptr(), free.numel(), top.data_ptr(), (top if top_out is None else top_out).data_ptr(),
+                     batch, lens.data_ptr(), _index(cache, counts, batch), _index(cache, granted, batch), tokens, slots.data_ptr(),
+                     _index(cache, positions, tokens), _index(cache, starts, batch + 1), _cache_stream(cache))
+    if rc:
+        raise WQError("wq_kv_reserve", rc)
+    return slots, positions, starts, granted
+
+
+def kv_release(cache, free, top, lens, keep=None, top_out=None, stream=None):
+    """The pages behind the first keep[b] tokens (None: all) of sequences that hold lens[b] go back on the stack that free and
+    top are (as in kv_reserve)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_release(cache, free, top, lens, keep, top_out)
+    batch = _turn(cache, free, top, top_out, lens)
+    rc = _kv_release(cache.ref, free.data_ptr(), free.numel(), top.data_ptr(), (top if top_out is None else top_out).data_ptr(),
+                     batch, lens.data_ptr(), _index(cache, keep, batch), _cache_stream(cache))
+    if rc:
+        raise WQError("wq_kv_release", rc)
+
+
+def _turn(cache, free, top, top_out, lens):
+    """Checks what kv_reserve and kv_release share -> the batch."""
+    batch = lens.numel()
+    assert cache.tensors[4] is not None and batch <= cache.batch, "the cache has no table, or not that many rows"
+    _index(cache, lens, batch)
+    _index(cache, free, free.numel())
+    _index(cache, top, 1)
+    _index(cache, top_out, 1)
+    return batch
+
+
+def kv_keep(cache, start, path, counts=None, stream=None):
+    """The rows at start[b] + path[b, i] move to start[b] + i, i < counts[b] (None: all): an accepted path of drafted nodes
+    behind the context.  start, counts: int32 [batch]; path: int32 [batch, n], n up to WQ_PATH_MAX."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_keep(cache, start, path, counts)
+    batch, n = path.shape
+    assert batch <= cache.batch
+    rc = _kv_keep(cache.ref, _index(cache, start, batch), batch, _index(cache, path, batch * n), n, _index(cache, counts, batch),
+                  _cache_stream(cache))
+    if rc:
+        raise WQError("wq_kv_keep", rc)
+
+
+def tree_mask(parents, counts=None, window=0, stream=None):
+    """What the nodes of drafted trees see of each other, for attend(tree=).  parents: int32 CUDA tensor [batch, tokens],
+    node i's parent (before it) or -1; counts: int32 [batch] nodes of each sequence (None: all).  Returns mask int32
+    [batch, tokens, ceil(tokens / 32)], whose bit j of node i is set for i itself and its ancestors (window > 0: at most
+    window - 1 levels up), and depth int32 [batch, tokens], the number of its ancestors."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_mask(parents, counts, window)
+    batch, tokens = parents.shape
+    index = torch._C._cuda_getDevice()
+    assert parents.get_device() == index and parents.dtype is torch.int32 and parents.is_contiguous()
+    assert counts is None or (counts.get_device() == index and counts.dtype is torch.int32 and counts.is_contiguous() and
+                              counts.numel() == batch)
+    mask = torch.empty((batch, tokens, (tokens + 31) // 32), dtype=torch.int32, device=parents.device)
+    depth = torch.empty((batch, tokens), dtype=torch.int32, device=parents.device)
+    rc = _tree_mask(parents.data_ptr(), batch, tokens, None if counts is None else counts.data_ptr(), window, mask.data_ptr(),
+                    depth.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise WQError("wq_tree_mask", rc)
+    return mask, depth
+
+
+def _rows(cache, t):
+    """[token, head, dim] view of bf16 -> the bytes of a wq_heads."""
+    st, sh, sd = t.stride()
+    assert t.get_device() == cache.index and t.dtype is torch.bfloat16 and sd == 1
+    return _pack_heads(t.data_ptr(), 0, st, sh)
+
+
+def _tree(cache, tree, batch, tokens):
+    """(mask, depth) as tree_mask gives them, or of one tree for all sequences ([1, ...]) -> the bytes of a wq_tree."""
+    mask, depth = tree
+    words = (tokens + 31) // 32
+    assert mask.get_device() == cache.index and mask.dtype is torch.int32 and mask.is_contiguous()
+    assert mask.shape[1:] == (tokens, words) and mask.shape[0] in (1, batch)
+    if depth is not None:
+        assert depth.get_device() == cache.index and depth.dtype is torch.int32 and depth.is_contiguous()
+        assert depth.shape[1:] == (tokens,) and depth.shape[0] in (1, batch)
+    return _pack_tree(mask.data_ptr(), 0 if depth is None else depth.data_ptr(), tokens * words if mask.shape[0] == batch else 0,
+                      tokens if depth is not None and depth.shape[0] == batch else 0)
+
+
 def attend_workspace_bytes(cache, batch, tokens, q_heads, max_len=0):
     return int(lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len))
 
 
 def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_len=0, out=None, out_f32=False,
-           return_lse=False, workspace=None, stream=None):
+           return_lse=False, workspace=None, stream=None, sinks=0, tree=None):
     """Attention of q (bf16 [batch, tokens, q_heads, dim] view) over the lens[b] cached tokens of each sequence.
 
     lens, counts: int32 CUDA tensors [batch]; the last counts[b] (None: all of `tokens`) cached positions are
@@ -363,10 +500,15 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
     default dim^-0.5.  max_len: a host-side upper bound of lens if one is known (plans the split of long
     sequences).  out: a [batch, tokens, q_heads, dim] view to write to.  Returns out, or (out, lse) with
     lse fp32 [batch, tokens, q_heads].  Rows that see nothing give 0 and -inf.  workspace: a uint8 tensor of
-    attend_workspace_bytes() bytes that no other call in flight uses; allocated for the call when None."""
+    attend_workspace_bytes() bytes that no other call in flight uses; allocated for the call when None.
+
+    sinks: the first `sinks` tokens stay visible behind a window.  tree: (mask, depth) of tree_mask, or of one tree for all
+    sequences: q's tokens are nodes of a draft, which see the tokens before the draft (a window and sinks as from
+    their depth) and of the draft what their mask says; depth None: node i is at depth i."""
     if stream is not None:                     # results and workspace are allocated on the stream that uses them
         with torch.cuda.stream(stream):
-            return attend(cache, q, lens, counts, causal, window, scale, max_len, out, out_f32, return_lse, workspace)
+            return attend(cache, q, lens, counts, causal, window, scale, max_len, out, out_f32, return_lse, workspace,
+                          None, sinks, tree)
     batch, tokens, q_heads, dim = q.shape
     assert dim == cache.dim and batch <= cache.batch
     dt = torch.float32 if out_f32 else torch.bfloat16
@@ -381,12 +523,16 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         assert workspace.get_device() == cache.index and workspace.dtype is torch.uint8 and workspace.is_contiguous()
-    rc = _attend(cache.ref, _heads(cache, q, torch.bfloat16), _heads(cache, out, dt), None if lse is None else lse.data_ptr(), batch,
-                 tokens, q_heads, _index(cache, lens, batch), _index(cache, counts, batch), max_len,
-                 dim ** -0.5 if scale is None else scale, window,
-                 (WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
-                 None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-                 _cache_stream(cache))
+    args = (cache.ref, _heads(cache, q, torch.bfloat16), _heads(cache, out, dt), None if lse is None else lse.data_ptr(), batch,
+            tokens, q_heads, _index(cache, lens, batch), _index(cache, counts, batch), max_len,
+            dim ** -0.5 if scale is None else scale, window)
+    rest = ((WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+            _cache_stream(cache))
+    if sinks or tree is not None:
+        rc = _attend_ex(*args, sinks, None if tree is None else _tree(cache, tree, batch, tokens), *rest)
+    else:
+        rc = _attend(*args, *rest)
     if rc:
         raise WQError("wq_attend", rc)
     return (out, lse) if return_lse else out

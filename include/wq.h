@@ -314,6 +314,71 @@ int wq_kv_append(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v,
 int wq_kv_read(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t batch, int64_t tokens,
                const int32_t* start, const int32_t* counts, unsigned flags, void* stream);
 
+/* wq_kv_append_slots: quantise the rows of `tokens` tokens laid end to end (a batch of unequal requests without
+ * padding; k->batch and v->batch are not used) into the cache, token i to slots[i] = page * page_size + offset, the
+ * form in which wq_kv_reserve gives them.  A token whose slot is negative is skipped; one past the cache's pages is
+ * too, and wq_last_device_status reports WQ_ERR_ARG.  The cache's table is not read.  Tokens of one call must not share
+ * a slot.  slots: 8-byte aligned.                                                */
+int wq_kv_append_slots(const wq_kv_cache* cache, const wq_heads* k, const wq_heads* v, int64_t tokens,
+                       const int64_t* slots, void* stream);
+
+/* ---------------------------------------------------------------- pages and slots of a changing batch
+ * The table of a cache, which all its layers may share, is kept on the device: free_pages[0 .. top) is a stack of page
+ * numbers that no sequence holds (room for free_size).  Sequence b holds ceil(lens[b] / page_size) pages; what its row
+ * of the table has behind them is not looked at.
+ *
+ * wq_kv_reserve: pages for counts[b] tokens behind the lens[b] of each sequence, in the order of the sequences, the
+ * stack's last page first, written to the table (which has to be writable).  A sequence whose pages the stack does not
+ * hold any more gets none, and so does one whose tokens would pass its capacity; behind the first that the stack fails,
+ * only those get their tokens that need no new page.  Outputs (each may be NULL, but top_out):
+ *   granted    [batch] counts[b], or 0 where the sequence got nothing: the counts of the following calls
+ *   starts     [batch + 1] where each sequence's tokens begin when all counts[b] are laid end to end (those that got
+ *              nothing too), and their sum
+ *   slots      [tokens] the slot of each of these tokens, -1 without one; -1 behind the last token
+ *   positions  [tokens] its position, lens[b] + i; 0 behind the last token
+ *   top_out    the pages that are left; may be `top` itself
+ * More tokens than `tokens` are not written, and wq_last_device_status reports WQ_ERR_ARG; so it does for a page number
+ * outside the cache (slot -1).  Negative lens and counts are taken for 0.  granted must not overlap counts.
+ *
+ * wq_kv_release: of each sequence's pages those behind its first keep[b] tokens (NULL: all of them) go back on the stack,
+ * in the order of the sequences and of their pages; those past its capacity are not there.  The table is not written.
+ * Pages that find no room on the stack are dropped, and wq_last_device_status reports WQ_ERR_ARG.
+ *
+ * batch <= WQ_TURN_MAX; slots 8-byte aligned, the others 4-byte.                 */
+#define WQ_TURN_MAX 65536
+int wq_kv_reserve(const wq_kv_cache* cache, const int32_t* free_pages, int64_t free_size, const int32_t* top,
+                  int32_t* top_out, int64_t batch, const int32_t* lens, const int32_t* counts, int32_t* granted,
+                  int64_t tokens, int64_t* slots, int32_t* positions, int32_t* starts, void* stream);
+int wq_kv_release(const wq_kv_cache* cache, int32_t* free_pages, int64_t free_size, const int32_t* top, int32_t* top_out,
+                  int64_t batch, const int32_t* lens, const int32_t* keep, void* stream);
+
+/* ---------------------------------------------------------------- trees of drafted tokens
+ * A draft is a tree of up to `tokens` nodes behind what a sequence holds, parents before their children: parents[b][i]
+ * is the number of node i's parent, or -1.  Its K and V are appended in the nodes' order.
+ *
+ * wq_tree_mask: mask [batch, tokens, ceil(tokens / 32)]: bit j of node i's words (bit j % 32 of word j / 32) is set where
+ * j is i or an ancestor of it; with window > 0 at most window - 1 levels up.  depth [batch, tokens] (or NULL): the number of
+ * its ancestors.  Both are 0 for nodes from counts[b] on (NULL: none).  A parent that does not come before its
+ * child is taken for -1, and wq_last_device_status reports WQ_ERR_ARG.  tokens <= WQ_TREE_MAX.
+ *
+ * wq_kv_keep: the rows of the nodes on an accepted path move up behind the context: position start[b] + path[b][i] to
+ * start[b] + i for i < counts[b] (NULL: path_ld; values outside [0, path_ld] are clamped), codes and scales bit for bit,
+ * all read before any is written.  path is [batch, path_ld], path_ld <= WQ_PATH_MAX.  A row whose position or place
+ * lies outside the cache stays, and wq_last_device_status reports WQ_ERR_ARG.  Sequences must not share the pages
+ * that are written.                                                               */
+#define WQ_TREE_MAX 1024
+#define WQ_PATH_MAX 512
+typedef struct wq_tree {
+  const uint32_t* mask;    /* as above; any bits may be set                                  */
+  const int32_t* depth;    /* NULL: node i is at depth i.  Only a window looks at it          */
+  int64_t mask_batch;      /* elements from one sequence's to the next: 0 for one tree for all */
+  int64_t depth_batch;
+} wq_tree;
+int wq_tree_mask(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window,
+                 uint32_t* mask, int32_t* depth, void* stream);
+int wq_kv_keep(const wq_kv_cache* cache, const int32_t* start, int64_t batch, const int32_t* path, int64_t path_ld,
+               const int32_t* counts, void* stream);
+
 /* ---------------------------------------------------------------- attention over the cache
  * wq_attend: out = softmax(scale * q . K^T) . V over the cached tokens, per
  * sequence and query head.  q is bf16 [batch, tokens, q_heads, dim]; q_heads is a
@@ -348,6 +413,19 @@ size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_
 int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
               int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
               float scale, int64_t window, unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* wq_attend_ex: wq_attend, and (WQ_FLAG_CAUSAL only)
+ *   sinks > 0     the first `sinks` tokens stay visible behind the window: 0 <= t <= p and (t > p - window or t < sinks).
+ *                 Without a window they change nothing.  What lies between them and the window is not read.
+ *   tree          (NULL: none; in HOST memory) the counts[b] query tokens are nodes of a draft.  Node i sees the context,
+ *                 t < lens[b] - counts[b], with a window and sinks as a token at lens[b] - counts[b] + depth[i]
+ *                 (clamped to 0 .. counts[b] - 1) does, and node j, at t = lens[b] - counts[b] + j, where bit j of its
+ *                 mask is set: itself too only then.  tokens <= WQ_TREE_MAX.
+ * The workspace is that of wq_attend.                                             */
+int wq_attend_ex(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
+                 int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
+                 float scale, int64_t window, int64_t sinks, const wq_tree* tree, unsigned flags, void* workspace,
+                 size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- status
  * wq_last_device_status: synchronises the current device, returns and clears

@@ -64,3 +64,56 @@ def attend(q, k, v, n_q, scale, causal, window=0):
             out[i, h], mean[i, h] = p @ vh, p @ np.abs(vh)
             top[i, h] = (abs(scale) * (np.abs(kh) @ np.abs(q[i, h]))).max()
     return out, lse, mean, top
+
+
+def ancestors(parents, n, window=0):
+    """Nodes 0 .. n-1 of a tree (parents[i] < i, or -1): bool [L, L], whether node i is or descends from j (window > 0: by
+    fewer than `window` levels), and depths [L]; nothing for nodes from n on."""
+    L = len(parents)
+    seen, depth = np.zeros((L, L), bool), np.zeros(L, np.int32)
+    for i in range(n):
+        j, up = i, 0
+        while j != -1:
+            seen[i, j] = window == 0 or up < window
+            j, up = int(parents[j]), up + 1
+        depth[i] = up - 1
+    return seen, depth
+
+
+def mask_words(seen):
+    """bool [..., L] -> int32 [..., ceil(L / 32)], bit j of the words for element j."""
+    L = seen.shape[-1]
+    wide = np.zeros(seen.shape[:-1] + (-(-L // 32) * 32,), np.uint8)
+    wide[..., :L] = seen
+    return np.packbits(wide, axis=-1, bitorder="little").view("<i4")
+
+
+def visible(L, n_q, T, window=0, sinks=0, nodes=None, depth=None):
+    """bool [L, T]: which of T cached tokens each of L query rows sees, the last n_q positions being the first n_q rows'.
+    nodes [L, L]: they are drafted nodes that see each other by it, at depths `depth` (None: in order)."""
+    seen, base = np.zeros((L, T), bool), T - n_q
+    for i in range(min(L, n_q)):
+        p = base + (i if depth is None or nodes is None else min(max(int(depth[i]), 0), n_q - 1))
+        for t in range(T):
+            near = window == 0 or t > p - window or t < sinks
+            seen[i, t] = nodes[i, t - base] if nodes is not None and t >= base else near and (nodes is not None or t <= p)
+    return seen
+
+
+def attend_seen(q, k, v, seen, scale):
+    """attend() for rows that see the tokens `seen` [L, T]; the same results."""
+    q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    L, Hq, D = q.shape
+    H = k.shape[1]
+    out, mean, lse, top = np.zeros((L, Hq, D)), np.zeros((L, Hq, D)), np.full((L, Hq), -np.inf), np.zeros((L, Hq))
+    some = seen.any(1)
+    for h in range(Hq if some.any() else 0):
+        kh, vh = k[:, h * H // Hq], v[:, h * H // Hq]
+        s = np.where(seen, scale * (q[:, h] @ kh.T), -np.inf)[some]
+        m = s.max(1, keepdims=True)
+        e = np.exp(s - m)
+        total = e.sum(1, keepdims=True)
+        lse[some, h] = (m + np.log(total))[:, 0]
+        out[some, h], mean[some, h] = e / total @ vh, e / total @ np.abs(vh)
+        top[some, h] = np.where(seen, abs(scale) * (np.abs(q[:, h]) @ np.abs(kh).T), 0)[some].max(1)
+    return out, lse, mean, top
