@@ -87,7 +87,7 @@ struct Plan {
   size_t slots;        // partial rows in the workspace
 };
 
-Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, int64_t window, int64_t sinks) {
+Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, int64_t window, int64_t sinks, bool sel) {
   Plan pl{};
   const int64_t group = q_heads / kv.heads, rows = tokens * group;
   // The window only ever lowers the number of parts, so that the workspace without it suffices (parts of 2048 tokens
@@ -102,9 +102,9 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     // SMs are left, four tiles of 128 to a part at least.
     const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
     pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
-    if (half == 1) pl.tcp.groups = 1;
+    if (half == 1 || sel) pl.tcp.groups = 1;
     pl.tcp.row_tiles = (int)((half + pl.tcp.groups - 1) / pl.tcp.groups);
-    const int64_t tiles = (seen + 127) / 128, most = (tiles + 3) / 4, room = kSms * (kv.dim == 64 && pl.tcp.groups == 1 ? 2 : 1);
+    const int64_t tiles = (seen + 127) / 128, most = (tiles + 3) / 4, room = kSms * ((kv.dim == 64 || sel) && pl.tcp.groups == 1 ? 2 : 1);
     int64_t want = room / (heads * pl.tcp.row_tiles);
     if (want > most) want = most;
     pl.tcp.parts = (int)(want > 1 ? want : 1);
@@ -153,12 +153,14 @@ int launch_join(const JoinParams& p, int tile_rows, cudaStream_t s) {
 }  // namespace
 
 size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len) {
-  return plan(kv, batch, tokens, q_heads, max_len, 0, 0).slots * ((size_t)kv.dim + 2) * sizeof(float);
+  const size_t plain = plan(kv, batch, tokens, q_heads, max_len, 0, 0, false).slots;
+  const size_t sel = plan(kv, batch, tokens, q_heads, max_len, 0, 0, true).slots;
+  return (plain > sel ? plain : sel) * ((size_t)kv.dim + 2) * sizeof(float);
 }
 
 int attend(const AttendArgs& a, cudaStream_t s) {
   const bool sel = a.tree_mask || (a.window > 0 && a.sinks > 0);
-  const Plan pl = plan(a.kv, a.batch, a.tokens, a.q_heads, a.max_len, a.window, sel ? a.sinks : 0);
+  const Plan pl = plan(a.kv, a.batch, a.tokens, a.q_heads, a.max_len, a.window, sel ? a.sinks : 0, sel);
   const int rc = pl.tc ? (sel ? attend_tc_sel : attend_tc)(a, pl.tcp, s) : (sel ? attend_few_sel : attend_few)(a, pl.few, s);
   if (rc != WQ_OK || pl.parts == 1) return rc;
   JoinParams p{};

@@ -189,14 +189,15 @@ struct Params {
   float* part_ml;   // [row tile][part][GROUPS * 128][2] their m (base 2) and l
 };
 
-template <int D, int GROUPS>
+template <int D, int GROUPS, bool SEL>
 struct Lay {
+  static constexpr int NB = SEL && D == 128 && GROUPS == 1 ? 1 : 2;   // buffers for tiles of K, and of V
   static constexpr int CH = D / 64;                       // 128-byte chunks of an operand row
   static constexpr int Q_OFF = 0;                         // [GROUPS][CH][128 rows][128 bytes]
   static constexpr int TB = CH * 128 * 128;               // bytes of a K or V tile [CH][128 tokens][128 bytes]
-  static constexpr int K_OFF = GROUPS * TB;               // two of them
-  static constexpr int V_OFF = K_OFF + 2 * TB;
-  static constexpr int MASK_OFF = V_OFF + 2 * TB;         // [4 tiles][4 warps] uint4 of marks
+  static constexpr int K_OFF = GROUPS * TB;               // NB of them
+  static constexpr int V_OFF = K_OFF + NB * TB;
+  static constexpr int MASK_OFF = V_OFF + NB * TB;         // [4 tiles][4 warps] uint4 of marks
   static constexpr int SUM_OFF = MASK_OFF + 4 * 4 * 16;   // [4 tiles][4 warps] bit 0: .x or .y, 1: .z, 2: .w has a mark
   static constexpr int BAR_OFF = SUM_OFF + 4 * 4 * 4;
   static constexpr int NBAR = 8 + 3 * GROUPS + 3;
@@ -212,9 +213,9 @@ struct Lay {
 
 // SEL: the rows may see the first tokens besides their window, or nodes of a tree (kv::sight).
 template <int FMT, int D, int GROUPS, bool SEL>
-__global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BLOCKS))
+__global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS, SEL>::BLOCKS))
     attend_tc_kernel(const __grid_constant__ Params p) {
-  using L = Lay<D, GROUPS>;
+  using L = Lay<D, GROUPS, SEL>;
   const AttendArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     fetch(row, raw);
     bool ok = true;
     for (int j = 0; j < tiles && ok; ++j) {
-      const int buf = j & 1;
+      const int buf = j % L::NB;
       // V scales that are no finite numbers become zeros, the token is marked
       bool bad = false;
 #pragma unroll
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         marks.z = __ballot_sync(0xFFFFFFFFu, kl != 0);
         marks.w = __ballot_sync(0xFFFFFFFFu, vl != 0);
       }
-      if (j >= 2 && !wait_all(&kempty[buf], ((j >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (j >= L::NB && !wait_all(&kempty[buf], ((j / L::NB) & 1) ^ 1, abort_flag)) { ok = false; break; }
       if (lane == 0) {
         reinterpret_cast<uint4*>(smem + L::MASK_OFF)[(j & 3) * 4 + dw] = marks;
         reinterpret_cast<uint32_t*>(smem + L::SUM_OFF)[(j & 3) * 4 + dw] =
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&kfull[buf]);
-      if (j >= 2 && !wait_all(&vempty[buf], ((j >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (j >= L::NB && !wait_all(&vempty[buf], ((j / L::NB) & 1) ^ 1, abort_flag)) { ok = false; break; }
       store(smem + L::V_OFF + buf * L::TB, raw.v, raw.vs, vl != 0);
       fence_proxy_async_smem();
       __syncwarp();
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     const uint64_t kd = smem_desc(smem_u32(smem + L::K_OFF), 16, 1024, 2);
     const uint64_t vd = smem_desc(smem_u32(smem + L::V_OFF), 16384, 1024, 2);   // D contiguous: 64 elements, then 16 KB on
     auto scores = [&](int g, int j) {
-      const uint64_t ad = qd + (uint64_t)(g * L::TB >> 4), bd = kd + (uint64_t)((j & 1) * L::TB >> 4);
+      const uint64_t ad = qd + (uint64_t)(g * L::TB >> 4), bd = kd + (uint64_t)((j % L::NB) * L::TB >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t at = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2);
@@ -641,9 +642,9 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
       commit_one(&kempty[0]);
     }
     for (int j = 0; j < tiles && ok; ++j) {
-      const int buf = j & 1;
+      const int buf = j % L::NB, next = (j + 1) % L::NB;
       for (int g = 0; g < groups && ok; ++g) {
-        if (g == 0 && !wait_all(&vfull[buf], (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (g == 0 && !wait_all(&vfull[buf], (j / L::NB) & 1, abort_flag)) { ok = false; break; }
         if (!wait_all(&pfull[g], j & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint64_t bd = vd + (uint64_t)(buf * L::TB >> 4);
@@ -653,10 +654,10 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
         commit_one(&ofull[g]);
         if (g == groups - 1) commit_one(&vempty[buf]);
         if (j + 1 < tiles) {
-          if (g == 0 && !wait_all(&kfull[buf ^ 1], ((j + 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (g == 0 && !wait_all(&kfull[next], ((j + 1) / L::NB) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           scores(g, j + 1);
-          if (g == groups - 1) commit_one(&kempty[buf ^ 1]);
+          if (g == groups - 1) commit_one(&kempty[next]);
         }
       }
     }
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
     wait_quiet(done, 0);
     if (tiles > 0) {
       if (*abort_flag) wait_quiet(drain, 0);
-      else wait_quiet(&vempty[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+      else wait_quiet(&vempty[(tiles - 1) % L::NB], ((tiles - 1) / L::NB) & 1);
     }
     tc_fence_after();
     tmem_dealloc(tmem, L::COLS);
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS>::THREADS), (Lay<D, GROUPS>::BL
 
 template <int FMT, int D, int GROUPS, bool SEL>
 int launch(const Params& p, cudaStream_t s) {
-  using L = Lay<D, GROUPS>;
+  using L = Lay<D, GROUPS, SEL>;
   static std::atomic<uint64_t> allowed{0};
   if (!allow_smem(allowed, attend_tc_kernel<FMT, D, GROUPS, SEL>, L::TOTAL)) return WQ_ERR_CUDA;
   const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.parts;

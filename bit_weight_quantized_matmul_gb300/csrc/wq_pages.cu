@@ -1,8 +1,8 @@
 // wq_pages.cu -- what a changing batch and drafted tokens ask of the 4-bit KV cache besides rows: pages and slots for
 // the tokens of a step, pages given back, the bits of trees, and the rows of an accepted path moved up.
 //
-// All of it is a few bytes a sequence, token or row, so a call costs its launch and its chain of dependent loads; each is
-// one launch, reads its lengths on the device and takes no workspace.
+// All of it is a few bytes a sequence, token or row, so a call costs its launch and its chain of dependent loads; lengths
+// are read on the device, and no call takes a workspace.
 #include <cuda_runtime.h>
 
 #include "wq_kv.cuh"
@@ -11,7 +11,8 @@ namespace wq {
 namespace {
 
 constexpr int kMost = 1024;      // threads of a block, and sequences of a round
-constexpr int kOwn = 4;          // tokens or pages that the thread of a sequence handles by itself
+constexpr int kSms = 152;
+constexpr int kShare = 2048;     // tokens or pages a block is launched for
 
 __device__ __forceinline__ int pages_for(const KvArgs& kv, int tokens) {   // ceil(tokens / page_size), tokens < 2^31
   return tokens > 0 ? kv::page_of(kv, tokens - 1) + 1 : 0;
@@ -58,160 +59,147 @@ __device__ __forceinline__ Sums block_scan(int64_t x, int64_t y, int64_t (*part)
   return r;
 }
 
-// What the warps have to know of a sequence that its thread does not handle by itself.
-struct Job {
-  int32_t b, len, n, have, need, ok;
-  int64_t first, start;          // its first page's place in the order of pages, its first token's
-};
+// The last i with key[i] <= x, 0 <= i < n; key[0] <= x, and the keys rise.
+__device__ __forceinline__ int last_at(const int32_t* key, int n, int x) {
+  int lo = 0;
+  for (int step = 1 << (31 - __clz(n)); step > 0; step >>= 1)
+    if (lo + step < n && key[lo + step] <= x) lo += step;
+  return lo;
+}
+
+__device__ __forceinline__ int clamp32(int64_t x) { return (int)min(x, (int64_t)0x7FFFFFFF); }
 
 // ---------------------------------------------------------------- pages and slots for the tokens of a step
-// A thread computes what its sequence needs, one scan over the sequences orders pages and tokens.  The blocks of the
-// cluster all do that (they would wait for one that did), and share the writing.  The stack's count may be read and written
-// at one address: every block has read it when the first one writes.
-__global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant__ KvReserveArgs a) {
+// A thread computes what its sequence needs, one scan over the sequences orders pages and tokens, and then a thread takes
+// a page or a token and looks up whose it is.  Every block does the scan (they would wait for one that did) and they share the
+// pages and tokens.  Where they read the stack's count from the address that it goes back to, a second launch writes it:
+// WRITE is all but the count.
+enum { WRITE = 1, COUNT = 2 };
+__global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant__ KvReserveArgs a, const int what) {
   __shared__ int64_t part[32][2];
-  __shared__ Job jobs[kMost];
-  __shared__ int count;
+  __shared__ int32_t first_of[kMost], start_of[kMost], len_of[kMost], have_of[kMost];   // have -1: no pages for it
+  __shared__ unsigned long long edge;              // pages that those before the first one without its pages take
   const KvArgs& kv = a.kv;
-  const int rank = (int)cluster_ctarank(), blocks = (int)(gridDim.x), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t pages = 0, tokens = 0;                   // of the sequences before this round's
   const int64_t top = min(max((int64_t)*a.top, (int64_t)0), a.free_size);
-  int64_t taken = 0;
-
-  // Page number of a sequence's page p, new ones from the stack.
-  auto page_at = [&](const Job& j, int p) -> int {
-    return p >= j.have ? a.free_pages[top - 1 - (j.first + (p - j.have))] : kv.table[j.b * kv.table_ld + p];
-  };
-  auto put_page = [&](const Job& j, int k) {
-    const int page = page_at(j, j.have + k);
-    if ((uint32_t)page >= (uint64_t)kv.pages) set_status(WQ_STATUS_ARG);
-    const_cast<int32_t*>(kv.table)[j.b * kv.table_ld + j.have + k] = page;
-  };
-  auto put_token = [&](const Job& j, int i) {
-    const int64_t k = j.start + i;
-    if (k >= a.tokens) return;
-    const int pos = (int)min((int64_t)j.len + i, (int64_t)0x7FFFFFFF);
-    int64_t slot = -1;
-    if (j.ok && a.slots) {
-      const int p = kv::page_of(kv, pos), page = page_at(j, p);
-      if ((uint32_t)page < (uint64_t)kv.pages) slot = (int64_t)page * kv.page_size + (pos - p * kv.page_size);
-      else set_status(WQ_STATUS_ARG);
-    }
-    if (a.slots) a.slots[k] = slot;
-    if (a.positions) a.positions[k] = pos;
-  };
+  int32_t* table = const_cast<int32_t*>(kv.table);
+  int64_t pages = 0, tokens = 0;                   // of the sequences before this round's
+  const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
+  if (what & WRITE) griddep_launch_dependents();
+  if (threadIdx.x == 0) edge = ~0ull;
 
   for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
-    if (threadIdx.x == 0) count = 0;
     const int64_t b = b0 + threadIdx.x;
-    Job j{};
+    int len = 0, n = 0, have = 0, need = 0;
+    bool ok = false;
     if (b < a.batch) {
-      j.b = (int)b;
-      j.len = max(a.lens[b], 0);
-      j.n = max(a.counts[b], 0);
-      const int64_t end = (int64_t)j.len + j.n;
-      j.ok = end <= kv.capacity;
-      if (j.ok) {
-        j.have = pages_for(kv, j.len);
-        j.need = pages_for(kv, (int)end) - j.have;
+      len = max(a.lens[b], 0);
+      n = max(a.counts[b], 0);
+      ok = (int64_t)len + n <= kv.capacity;
+      if (ok) {
+        have = pages_for(kv, len);
+        need = pages_for(kv, len + n) - have;
       }
     }
-    const Sums s = block_scan(j.need, j.n, part);
-    j.first = pages + s.x;
-    j.start = tokens + s.y;
-    if (j.need > 0 && j.first + j.need > top) j.ok = 0;
-    if (j.ok && j.need > 0) taken = j.first + j.need;
-    const int n = j.n;
-    j.n = (int)min((int64_t)j.n, max(a.tokens - j.start, (int64_t)0));   // those that have a place in the map
-    const int need = j.ok ? j.need : 0;
-    if (b < a.batch) {
-      if (rank == 0) {
-        if (a.granted) a.granted[b] = j.ok ? n : 0;
-        if (a.starts) a.starts[b] = (int32_t)min(j.start, (int64_t)0x7FFFFFFF);
+    const Sums s = block_scan(need, n, part);
+    const int64_t first = pages + s.x, start = tokens + s.y;
+    if (need > 0 && first + need > top) {
+      ok = false;
+      atomicMin(&edge, (unsigned long long)first);
+    }
+    if (what & WRITE) {
+      if (b < a.batch && blockIdx.x == 0) {
+        if (a.granted) a.granted[b] = ok ? n : 0;
+        if (a.starts) a.starts[b] = clamp32(start);
       }
-      if (need <= kOwn && j.n <= kOwn) {
-        if (rank == 0) {
-          for (int k = 0; k < need; ++k) put_page(j, k);
-          for (int i = 0; i < j.n; ++i) put_token(j, i);
+      first_of[threadIdx.x] = clamp32(first);
+      start_of[threadIdx.x] = clamp32(start);
+      len_of[threadIdx.x] = len;
+      have_of[threadIdx.x] = ok ? have : -1;
+      __syncthreads();
+      const int seqs = (int)min((int64_t)blockDim.x, a.batch - b0);
+      const int64_t end = (int64_t)min((unsigned long long)(pages + s.all_x), edge);
+      for (int64_t e = pages + me; e < end; e += all) {
+        const int i = last_at(first_of, seqs, (int)e);
+        const int page = a.free_pages[top - 1 - e];
+        if ((uint32_t)page >= (uint64_t)kv.pages) set_status(WQ_STATUS_ARG);
+        table[(b0 + i) * kv.table_ld + have_of[i] + ((int)e - first_of[i])] = page;
+      }
+      const int64_t stop = min(tokens + s.all_y, a.tokens);
+#pragma unroll 2
+      for (int64_t k = tokens + me; k < stop; k += all) {
+        const int i = last_at(start_of, seqs, (int)k);
+        const int pos = clamp32((int64_t)len_of[i] + ((int)k - start_of[i])), have = have_of[i];
+        if (a.slots) {
+          int64_t slot = -1;
+          if (have >= 0) {
+            const int p = kv::page_of(kv, pos);    // a new page's number is still on the stack
+            const int page = p >= have ? a.free_pages[top - 1 - ((int64_t)first_of[i] + (p - have))] : table[(b0 + i) * kv.table_ld + p];
+            if ((uint32_t)page < (uint64_t)kv.pages) slot = (int64_t)page * kv.page_size + (pos - p * kv.page_size);
+            else set_status(WQ_STATUS_ARG);
+          }
+          a.slots[k] = slot;
         }
-      } else {
-        j.need = need;
-        jobs[atomicAdd(&count, 1)] = j;            // their order does not matter
+        if (a.positions) a.positions[k] = pos;
       }
+      __syncthreads();
     }
-    __syncthreads();
-    // Warps of all blocks take pieces of 32 tokens in turn.
-    const int wide = (int)(blockDim.x >> 5);
-    for (int at = warp; at < count; at += wide) {
-      const Job w = jobs[at];
-      for (int k = rank * 32 + lane; k < w.need; k += 32 * blocks) put_page(w, k);
-#pragma unroll 4
-      for (int i = rank * 32 + lane; i < w.n; i += 32 * blocks) put_token(w, i);
-    }
-    __syncthreads();
     pages += s.all_x;
     tokens += s.all_y;
   }
-  if (rank == 0 && threadIdx.x == 0) {
-    if (a.starts) a.starts[a.batch] = (int32_t)min(tokens, (int64_t)0x7FFFFFFF);
-    if (a.tokens > 0 && tokens > a.tokens) set_status(WQ_STATUS_ARG);
+  if (what & WRITE) {
+    if (me == 0) {
+      if (a.starts) a.starts[a.batch] = clamp32(tokens);
+      if (a.tokens > 0 && tokens > a.tokens) set_status(WQ_STATUS_ARG);
+    }
+    for (int64_t k = tokens + me; k < a.tokens; k += all) {
+      if (a.slots) a.slots[k] = -1;
+      if (a.positions) a.positions[k] = 0;
+    }
   }
-  for (int64_t k = tokens + rank * (int)blockDim.x + threadIdx.x; k < a.tokens; k += (int64_t)blocks * blockDim.x) {
-    if (a.slots) a.slots[k] = -1;
-    if (a.positions) a.positions[k] = 0;
-  }
-  // The pages taken: the largest of the block's threads (those that got none are behind those that did).
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) taken = max(taken, __shfl_xor_sync(0xFFFFFFFFu, taken, d));
-  if (lane == 0) part[warp][0] = taken;
-  if (blocks > 1) cluster_sync();                  // every block has read the count
-  else __syncthreads();
-  if (rank == 0 && threadIdx.x == 0) {
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, part[w][0]);
-    *a.top_out = (int32_t)(top - taken);
-  }
+  if (!(what & COUNT) || blockIdx.x != 0) return;
+  if (!(what & WRITE)) griddep_wait();             // the launch before has read the count
+  __syncthreads();
+  if (threadIdx.x == 0) *a.top_out = (int32_t)(top - (int64_t)min((unsigned long long)pages, edge));
 }
 
 // ---------------------------------------------------------------- pages given back
-__global__ void __launch_bounds__(kMost) kv_release_kernel(const __grid_constant__ KvReserveArgs a) {
+// The same for the pages that go: `counts` are the tokens that stay.
+__global__ void __launch_bounds__(kMost) kv_release_kernel(const __grid_constant__ KvReserveArgs a, const int what) {
   __shared__ int64_t part[32][2];
-  __shared__ Job jobs[kMost];
-  __shared__ int count;
+  __shared__ int32_t first_of[kMost], have_of[kMost];
   const KvArgs& kv = a.kv;
-  const int rank = (int)cluster_ctarank(), blocks = (int)gridDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t top = min(max((int64_t)*a.top, (int64_t)0), a.free_size);
+  const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
   int64_t pages = 0;
-  auto push = [&](const Job& j, int k) {
-    const int64_t at = top + j.first + k;
-    if (at < a.free_size) const_cast<int32_t*>(a.free_pages)[at] = kv.table[j.b * kv.table_ld + j.have + k];
-  };
+  if (what & WRITE) griddep_launch_dependents();
   for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
-    if (threadIdx.x == 0) count = 0;
     const int64_t b = b0 + threadIdx.x;
-    Job j{};
+    int have = 0, need = 0;
     if (b < a.batch) {
-      j.b = (int)b;
-      j.len = (int)min((int64_t)max(a.lens[b], 0), kv.capacity);
-      j.have = min(pages_for(kv, j.len), pages_for(kv, a.counts ? max(a.counts[b], 0) : 0));   // pages that stay
-      j.need = pages_for(kv, j.len) - j.have;
+      const int held = pages_for(kv, (int)min((int64_t)max(a.lens[b], 0), kv.capacity));
+      have = min(held, pages_for(kv, a.counts ? max(a.counts[b], 0) : 0));
+      need = held - have;
     }
-    const Sums s = block_scan(j.need, 0, part);
-    j.first = pages + s.x;
-    if (j.need > kOwn) jobs[atomicAdd(&count, 1)] = j;
-    else if (rank == 0)
-      for (int k = 0; k < j.need; ++k) push(j, k);
-    __syncthreads();
-    const int wide = (int)(blockDim.x >> 5);
-    for (int at = warp; at < count; at += wide) {
-      const Job w = jobs[at];
-#pragma unroll 4
-      for (int k = rank * 32 + lane; k < w.need; k += 32 * blocks) push(w, k);
+    const Sums s = block_scan(need, 0, part);
+    if (what & WRITE) {
+      first_of[threadIdx.x] = clamp32(pages + s.x);
+      have_of[threadIdx.x] = have;
+      __syncthreads();
+      const int seqs = (int)min((int64_t)blockDim.x, a.batch - b0);
+      const int64_t end = min(pages + s.all_x, a.free_size - top);
+#pragma unroll 2
+      for (int64_t e = pages + me; e < end; e += all) {
+        const int i = last_at(first_of, seqs, (int)e);
+        const_cast<int32_t*>(a.free_pages)[top + e] = kv.table[(b0 + i) * kv.table_ld + have_of[i] + ((int)e - first_of[i])];
+      }
+      __syncthreads();
     }
-    __syncthreads();
     pages += s.all_x;
   }
-  if (blocks > 1) cluster_sync();                  // every block has read the count
-  if (rank == 0 && threadIdx.x == 0) {
+  if (!(what & COUNT) || blockIdx.x != 0) return;
+  if (!(what & WRITE)) griddep_wait();             // the launch before has read the count
+  __syncthreads();
+  if (threadIdx.x == 0) {
     if (top + pages > a.free_size) set_status(WQ_STATUS_ARG);
     *a.top_out = (int32_t)min(top + pages, a.free_size);
   }
@@ -294,21 +282,26 @@ int launched() {
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
+// work: tokens or pages, at most.
 template <class Kernel>
 int launch_turn(Kernel* kernel, const KvReserveArgs& a, int64_t work, cudaStream_t s) {
+  const int64_t wide = (a.batch + 31) / 32 * 32, want = (work + kShare - 1) / kShare;
+  const int blocks = want > kSms ? kSms : want < 1 ? 1 : (int)want;
+  const int threads = blocks > 1 || wide > kMost ? kMost : wide < 128 ? 128 : (int)wide;
+  const bool once = blocks == 1 || a.top_out != a.top;
+  kernel<<<blocks, threads, 0, s>>>(a, once ? WRITE | COUNT : WRITE);
+  int rc = launched();
+  if (rc != WQ_OK || once) return rc;
   cudaLaunchConfig_t cfg{};
-  const int64_t wide = (a.batch + 31) / 32 * 32;
-  const bool large = work > 4096;
-  cfg.gridDim = dim3(large ? 8 : 1);
-  cfg.blockDim = dim3((unsigned)(large || wide > kMost ? kMost : wide < 128 ? 128 : wide));
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = large ? 8 : 1;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return WQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, a, (int)COUNT) != cudaSuccess) return WQ_ERR_CUDA;
   return launched();
 }
 
