@@ -196,6 +196,14 @@ bool too_many(int64_t batch, int64_t tokens) {
   return batch > 0x7FFFFFFF || tokens > 0x7FFFFFFF || batch * tokens > 0x7FFFFFFF;
 }
 
+size_t workspace_bytes_of(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, bool sel) {
+  KvArgs kv{};
+  if (check_cache(cache, kv) != WQ_OK || batch <= 0 || tokens <= 0 || too_many(batch, tokens) || max_len < 0 ||
+      q_heads <= 0 || q_heads > 65535 || q_heads % kv.heads != 0)
+    return 0;
+  return attend_workspace(kv, batch, tokens, q_heads, max_len, sel);
+}
+
 // The part of a reserve or release call that the two share.
 int check_turn(const wq_kv_cache* cache, const int32_t* free_pages, int64_t free_size, const int32_t* top, int32_t* top_out,
                int64_t batch, const int32_t* lens, KvReserveArgs& a) {
@@ -508,11 +516,14 @@ int wq_tree_mask(const int32_t* parents, int64_t batch, int64_t tokens, const in
 
 size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
                                  int64_t max_len) {
-  KvArgs kv{};
-  if (check_cache(cache, kv) != WQ_OK || batch <= 0 || tokens <= 0 || too_many(batch, tokens) || max_len < 0 ||
-      q_heads <= 0 || q_heads > 65535 || q_heads % kv.heads != 0)
-    return 0;
-  return attend_workspace(kv, batch, tokens, q_heads, max_len);
+  return workspace_bytes_of(cache, batch, tokens, q_heads, max_len, false);
+}
+
+size_t wq_attend_ex_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
+                                    int64_t max_len) {
+  const size_t plain = workspace_bytes_of(cache, batch, tokens, q_heads, max_len, false);
+  const size_t sel = workspace_bytes_of(cache, batch, tokens, q_heads, max_len, true);
+  return plain > sel ? plain : sel;
 }
 
 int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
@@ -551,7 +562,7 @@ int wq_attend_ex(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* ou
   if (!lens) return WQ_ERR_ARG;
   if (((uintptr_t)lens & 3u) || ((uintptr_t)counts & 3u) || ((uintptr_t)lse & 3u)) return WQ_ERR_ALIGN;
   if ((rc = check_heads(q, 2, a.q)) != WQ_OK || (rc = check_heads(out, a.f32 ? 4 : 2, a.out)) != WQ_OK) return rc;
-  const size_t need = attend_workspace(a.kv, batch, tokens, q_heads, max_len);
+  const size_t need = attend_workspace(a.kv, batch, tokens, q_heads, max_len, tree || (window > 0 && sinks > 0));
   if (need > 0 && (!workspace || workspace_bytes < need)) return WQ_ERR_ARG;
   if (need > 0 && !aligned16(workspace)) return WQ_ERR_ALIGN;
   a.lse = lse;

@@ -102,7 +102,7 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     // SMs are left, four tiles of 128 to a part at least.
     const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
     pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
-    if (half == 1 || sel) pl.tcp.groups = 1;
+    if (half == 1) pl.tcp.groups = 1;
     pl.tcp.row_tiles = (int)((half + pl.tcp.groups - 1) / pl.tcp.groups);
     const int64_t tiles = (seen + 127) / 128, most = (tiles + 3) / 4, room = kSms * ((kv.dim == 64 || sel) && pl.tcp.groups == 1 ? 2 : 1);
     int64_t want = room / (heads * pl.tcp.row_tiles);
@@ -152,10 +152,8 @@ int launch_join(const JoinParams& p, int tile_rows, cudaStream_t s) {
 
 }  // namespace
 
-size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len) {
-  const size_t plain = plan(kv, batch, tokens, q_heads, max_len, 0, 0, false).slots;
-  const size_t sel = plan(kv, batch, tokens, q_heads, max_len, 0, 0, true).slots;
-  return (plain > sel ? plain : sel) * ((size_t)kv.dim + 2) * sizeof(float);
+size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, bool sel) {
+  return plan(kv, batch, tokens, q_heads, max_len, 0, 0, sel).slots * ((size_t)kv.dim + 2) * sizeof(float);
 }
 
 int attend(const AttendArgs& a, cudaStream_t s) {

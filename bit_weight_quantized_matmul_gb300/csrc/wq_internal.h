@@ -204,7 +204,7 @@ struct AttendArgs {
   const int32_t* tree_depth;    // NULL: node i is at depth i
   int64_t mask_batch, depth_batch;
 };
-size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len);
+size_t attend_workspace(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int64_t max_len, bool sel);
 int attend(const AttendArgs& a, cudaStream_t s);
 int take_status_attend();
 // Few query rows per cached head (wq_attend_few.cuh; 8 * nt of them): blocks of a cluster, or parts joined afterwards, share

@@ -95,6 +95,7 @@ _SIGS = {
     "wq_attend_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64, _I64, _I64]),
     "wq_attend": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I64, _U, _P,
                        ctypes.c_size_t, _P]),
+    "wq_attend_ex_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64, _I64, _I64]),
     "wq_attend_ex": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I64, _I64, _P, _U, _P,
                           ctypes.c_size_t, _P]),
     "wq_kv_append_slots": (_I, [_P, _P, _P, _I64, _P, _P]),
@@ -308,6 +309,7 @@ _pack_heads = struct.Struct("Pqqq").pack
 _kv_append, _kv_read = lib.wq_kv_append, lib.wq_kv_read
 _attend, _attend_workspace = lib.wq_attend, lib.wq_attend_workspace_bytes
 _pack_tree = struct.Struct("PPqq").pack
+_attend_ex_workspace = lib.wq_attend_ex_workspace_bytes
 _attend_ex, _kv_append_slots, _kv_keep, _tree_mask = lib.wq_attend_ex, lib.wq_kv_append_slots, lib.wq_kv_keep, lib.wq_tree_mask
 _kv_reserve, _kv_release = lib.wq_kv_reserve, lib.wq_kv_release
 
@@ -487,8 +489,10 @@ def _tree(cache, tree, batch, tokens):
                       tokens if depth is not None and depth.shape[0] == batch else 0)
 
 
-def attend_workspace_bytes(cache, batch, tokens, q_heads, max_len=0):
-    return int(lib.wq_attend_workspace_bytes(cache.ref, batch, tokens, q_heads, max_len))
+def attend_workspace_bytes(cache, batch, tokens, q_heads, max_len=0, select=False):
+    """Bytes of workspace that attend() needs; select: with sinks= or tree= too."""
+    need = _attend_ex_workspace if select else _attend_workspace
+    return int(need(cache.ref, batch, tokens, q_heads, max_len))
 
 
 def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_len=0, out=None, out_f32=False,
@@ -518,7 +522,7 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
         assert out.shape == q.shape
     lse = torch.empty((batch, tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
-        need = _attend_workspace(cache.ref, batch, tokens, q_heads, max_len)
+        need = (_attend_ex_workspace if sinks or tree is not None else _attend_workspace)(cache.ref, batch, tokens, q_heads, max_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:

@@ -421,7 +421,9 @@ int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, 
  *                 t < lens[b] - counts[b], with a window and sinks as a token at lens[b] - counts[b] + depth[i]
  *                 (clamped to 0 .. counts[b] - 1) does, and node j, at t = lens[b] - counts[b] + j, where bit j of its
  *                 mask is set: itself too only then.  tokens <= WQ_TREE_MAX.
- * The workspace is that of wq_attend.                                             */
+ * workspace: wq_attend_ex_workspace_bytes(...) bytes, enough with and without sinks and trees; as above.   */
+size_t wq_attend_ex_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
+                                    int64_t max_len);
 int wq_attend_ex(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, float* lse, int64_t batch,
                  int64_t tokens, int64_t q_heads, const int32_t* lens, const int32_t* counts, int64_t max_len,
                  float scale, int64_t window, int64_t sinks, const wq_tree* tree, unsigned flags, void* workspace,

@@ -104,6 +104,24 @@ def test_long_sequences_and_shared_tokens(fmt):
 
 
 @FMTS
+@pytest.mark.parametrize("tokens,hq,h,D,batch", [(1, 8, 8, 64, 31), (1, 32, 8, 128, 40), (3, 16, 4, 128, 40), (7, 12, 3, 64, 60), (2, 7, 7, 128, 129)])
+@pytest.mark.parametrize("longest", [20, 150, 700])
+def test_many_sequences_of_very_unequal_lengths(fmt, tokens, hq, h, D, batch, longest):
+    """More items than places: runs that begin and end inside items, items of many runs, sequences of nothing between them."""
+    need_gpu()
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 1 + longest // 8, batch)]
+    lens[batch // 3], lens[-1], lens[batch // 2] = longest, longest - 3, 0
+    counts = [int(x) for x in rng.integers(0, tokens + 1, batch)]
+    check(Case(78, fmt, h, D, batch, longest, 16), tokens, hq, lens, window=longest // 2, sinks=5)
+    case = Case(79, fmt, h, D, batch, longest, 32)
+    nodes, depth = zip(*(OK.ancestors(p, tokens) for p in random_trees(case.rng, batch, tokens)))
+    lens = [max(x, tokens) for x in lens]
+    check(case, tokens, hq, lens, counts, nodes=np.stack(nodes), depth=np.stack(depth))
+    check(case, tokens, hq, lens, counts, window=max(3, longest // 3), sinks=70, nodes=np.stack(nodes), depth=np.stack(depth))
+
+
+@FMTS
 @pytest.mark.parametrize("tokens", [1, 5, 140])
 def test_tokens_between_sinks_and_window_are_not_read(fmt, tokens):
     """Their pages hold NaN, or are not there at all: nothing changes, nothing is reported."""
@@ -212,7 +230,7 @@ def test_other_streams_graphs_and_workspaces(fmt, tokens, hq, n):
     q = bf16(case.rng, 2, tokens, hq, 128).cuda()
     parents = cuda(random_trees(case.rng, 2, tokens))
     args = dict(counts=counts, window=n // 2, sinks=40)
-    ws = torch.full((max(16, m.attend_workspace_bytes(cache, 2, tokens, hq)),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(16, m.attend_workspace_bytes(cache, 2, tokens, hq, select=True)),), 0xFF, dtype=torch.uint8, device="cuda")
     step = lambda **kw: m.attend(cache, q, lens, tree=m.tree_mask(parents, counts, window=n // 2), **args, **kw)  # noqa: E731
     want = step().clone()
     side = torch.cuda.Stream()
