@@ -82,6 +82,7 @@ struct Params {
   int group;        // query heads per cached head
   int cluster;      // blocks of a cluster, which share the tokens of a cached head (or 1)
   int parts;        // or blocks that do, joined by the join kernel (or 1)
+  bool sorted;      // SEL: the sequences that see most first
   float* part_o;    // [row tile][part][row][D] unnormalised outputs
   float* part_ml;   // [row tile][part][row][2] their m (base 2) and l
 };
@@ -180,9 +181,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   const int splits = p.cluster * p.parts;   // one of them is 1
   const int split = x % splits;         // the blocks of a cluster are neighbours
   x /= splits;
-  const int64_t item = x;               // (sequence, cached head)
   const int h = x % a.kv.heads;
-  const int64_t b = x / a.kv.heads;
+  int64_t b = x / a.kv.heads;
+  if (SEL && p.sorted) b = kv::by_length<32 * kWarps>(a, (int)b, reinterpret_cast<int*>(smem));
+  const int64_t item = b * a.kv.heads + h;
 
   // Q is asked for first: its addresses need nothing that is still on its way.  Lane (g, q) holds row
   // 8 j + g's elements 32 blk + 8 q .. + 7 (rows past counts[b] too: they are there, and their columns unused).
@@ -901,6 +903,7 @@ int launch_few(const AttendArgs& a, const AttendFewPlan& pl, cudaStream_t s) {
   p.group = (int)(a.q_heads / a.kv.heads);
   p.cluster = pl.cluster;
   p.parts = pl.parts;
+  p.sorted = SEL && a.batch > 1 && a.batch <= kv::kSorted && a.batch * a.kv.heads * pl.cluster * pl.parts > kSms * blocks_per_sm(pl.nt);
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = p.part_o + pl.slots * a.kv.dim;
   if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? launch_nt<WQ_Q4_0, 64, SEL>(p, pl.nt, s) : launch_nt<WQ_Q4_0, 128, SEL>(p, pl.nt, s);

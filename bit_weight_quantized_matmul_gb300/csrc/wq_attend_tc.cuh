@@ -50,6 +50,7 @@ using kv::mul2;
 using kv::pack_f16x2;
 
 constexpr int kTile = 128;      // tokens of a tile
+constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;  // how far (base 2) a score may pass m before m moves
 constexpr float kUp = 11.0f;    // P = 2^(score - m + kUp): at most 2^15, and exact to 11 bits down to 2^-25 of the largest
@@ -185,9 +186,15 @@ struct Params {
   int group;        // query heads per cached head
   int row_tiles;    // blocks of GROUPS * 128 query rows per cached head
   int parts;        // blocks that share the tokens of one of them
+  bool sorted;      // SEL: the sequences that see most first
   float* part_o;    // [row tile][part][GROUPS * 128][D] unnormalised outputs
   float* part_ml;   // [row tile][part][GROUPS * 128][2] their m (base 2) and l
 };
+
+// The token of a row, by a 32-bit division where that does.
+__device__ __forceinline__ int64_t row_token(int64_t r, int group) {
+  return r >> 32 ? r / group : (int64_t)((uint32_t)r / (uint32_t)group);
+}
 
 template <int D, int GROUPS, bool SEL>
 struct Lay {
@@ -241,8 +248,27 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
   const int rt = p.row_tiles - 1 - (int)(x % p.row_tiles);
   x /= p.row_tiles;
   const int h = x % a.kv.heads;
-  const int64_t b = x / a.kv.heads;
+  int64_t b = x / a.kv.heads;
+  if (SEL && p.sorted) b = kv::by_length<L::THREADS>(a, (int)b, reinterpret_cast<int*>(smem));
 
+  // Q's rows as they are to their places, D / 8 lanes a row, while the lengths are still on their way; the softmax threads scale
+  // their own rows there.  (Read from global memory by its thread, a row took 5 us of a block's beginning: 32 lines a load.)
+  if (warp < L::SOFT) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int e = lane % kLanes;
+    const int64_t r_w = (int64_t)rt * GROUPS * 128 + warp * 32, i_w = row_token(r_w, p.group);
+    const uint32_t rest = (uint32_t)(r_w - i_w * p.group);
+    const uint16_t* q0 = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + (int64_t)h * p.group * a.q.head + 8 * e;
+    const uint32_t to = smem_u32(smem + L::Q_OFF + (warp >> 2) * L::TB + (warp & 3) * 32 * 128 + (e >> 3) * 16384);
+#pragma unroll 4
+    for (int x = lane / kLanes; x < 32; x += kRows) {
+      const uint32_t up = (rest + x) / (uint32_t)p.group;
+      const bool in = i_w + up < a.tokens;
+      const uint16_t* src = q0 + (in ? (i_w + up) * a.q.token + (int64_t)(rest + x - up * (uint32_t)p.group) * a.q.head : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + x * 128 + (((e & 7) ^ (x & 7)) << 4)), "l"(src),
+                   "r"(in ? 16 : 0) : "memory");
+    }
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 4);
@@ -296,7 +322,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
   if (warp < L::SOFT) {
     // ---------------------------------------------------------------- softmax: thread = query row
     const int grp = warp >> 2;
-    const int64_t r = r0 + threadIdx.x, i = r / p.group;            // softmax warps come first: threadIdx.x < 128 GROUPS
+    const int64_t r = r0 + threadIdx.x, i = row_token(r, p.group);            // softmax warps come first: threadIdx.x < 128 GROUPS
     const int hq = h * p.group + (int)(r - i * p.group);
     const bool mine = r < rows;
     const int lo = mine ? lo_of(i) : 0, hi = mine ? hi_of(i) : 0x7FFFFFFF;   // what is no row need not be masked
@@ -306,14 +332,17 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
     const uint32_t o_at = tmem + ((uint32_t)(warp & 3) << 21) + GROUPS * 128 + grp * D;
     float fac = 0.0f, m = -INFINITY, l = 0.0f;
     bool ok = true;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();                             // the warp's rows of Q have come in as they are
     if (tiles > 0 && grp < groups) {
       // Q: the row times 2^e with its largest element in 2^12 .. 2^13, fp16, and with the signs of the scale and of g: the
       // largest score has to be the largest product
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + b * a.q.batch + i * a.q.token + hq * a.q.head;
+      uint8_t* row = smem + L::Q_OFF + grp * L::TB + (threadIdx.x & 127) * 128;
+      auto chunk = [&](int e) { return reinterpret_cast<uint4*>(row + (e >> 3) * 16384 + (((e & 7) ^ (threadIdx.x & 7)) << 4)); };
       float amax = 0.0f;
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
-        const uint4 w = mine ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
+        const uint4 w = mine ? *chunk(e) : make_uint4(0, 0, 0, 0);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(bf16_bits_to_f32((u[k >> 1] >> (16 * (k & 1))) & 0xFFFFu)));
@@ -323,10 +352,9 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
       const float kg = FMT == WQ_NVFP4 && a.kv.g[0] ? *a.kv.g[0] : 1.0f;
       const float up = copysignf(__uint_as_float((uint32_t)(127 + e2) << 23), a.scale) * copysignf(1.0f, kg);
       fac = fabsf(a.scale) * kLog2e * fabsf(kg) * __uint_as_float((uint32_t)(127 - e2) << 23);
-      uint8_t* row = smem + L::Q_OFF + grp * L::TB + (threadIdx.x & 127) * 128;
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
-        const uint4 w = mine ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
+        const uint4 w = mine ? *chunk(e) : make_uint4(0, 0, 0, 0);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         float v[8];
 #pragma unroll
@@ -334,8 +362,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
           const int el = octet<FMT>(k);
           v[k] = bf16_bits_to_f32((u[el >> 1] >> (16 * (el & 1))) & 0xFFFFu) * up;
         }
-        *reinterpret_cast<uint4*>(row + (e >> 3) * 16384 + (((e & 7) ^ (threadIdx.x & 7)) << 4)) =
-            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        *chunk(e) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
       }
     }
     fence_proxy_async_smem();
@@ -702,6 +729,8 @@ int launch_tc(const AttendArgs& a, const AttendTcPlan& pl, cudaStream_t s) {
   p.group = (int)(a.q_heads / a.kv.heads);
   p.row_tiles = pl.row_tiles;
   p.parts = pl.parts;
+  p.sorted = SEL && a.batch > 1 && a.batch <= kv::kSorted &&
+             a.batch * a.kv.heads * pl.row_tiles * pl.parts > kSms * (pl.groups == 1 ? 2 : 1);
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = p.part_o + pl.slots * a.kv.dim;
   if (a.kv.fmt == WQ_Q4_0) return a.kv.dim == 64 ? launch_g<WQ_Q4_0, 64, SEL>(p, pl.groups, s) : launch_g<WQ_Q4_0, 128, SEL>(p, pl.groups, s);

@@ -118,6 +118,35 @@ __device__ __forceinline__ uint32_t sight(int t0, int lo, int hi, int sinks, con
   return see;
 }
 
+// Which sequence sees the rank'th most tokens (of equals the lower number first): where there are more blocks than places, those
+// with the most to do begin first.  64 sequences of 8 heads behind a window of 4096 are 512 blocks for 456 places: the last 56
+// began after 23 .. 42 us of 87, most of them as long as any.  Lengths are on the device, so the host cannot order them.
+// batch <= kSorted; all threads of the block; room: batch ints and one in shared memory.
+constexpr int kSorted = 256;
+template <int THREADS>
+__device__ __forceinline__ int64_t by_length(const AttendArgs& a, int rank, int* room) {
+  const int batch = (int)a.batch;
+  for (int b = threadIdx.x; b < batch; b += THREADS) {
+    const int n = count_of(a.counts, b, a.tokens), len = max(a.lens[b], 0), held = (int)min((int64_t)len, a.kv.capacity);
+    const int lo = a.window ? (int)min((int64_t)held, max((int64_t)0, (int64_t)len - n - a.window + 1)) : 0;
+    room[b] = n > 0 ? held - lo + (a.window ? min(a.sinks, lo) : 0) : 0;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < batch; b += THREADS) {
+    const int mine = room[b];
+    int before = 0;
+    for (int c = 0; c < batch; ++c) {
+      const int other = room[c];
+      before += other > mine || (other == mine && c < b);
+    }
+    if (before == rank) room[batch] = b;
+  }
+  __syncthreads();
+  const int b = room[batch];
+  __syncthreads();                                 // `room` is free again
+  return b;
+}
+
 // ---- arithmetic of the attention kernels
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
