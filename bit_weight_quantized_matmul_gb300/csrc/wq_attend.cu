@@ -119,6 +119,17 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   const int64_t tiles = (seen + tile - 1) / tile, most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
   int64_t want = (int64_t)kSms * blocks_per_sm(pl.few.nt) / (blocks > 0 ? blocks : 1);
   if (want > most) want = most;
+  // More items than half of the places: each of long sequences in two parts, in the order of by_length, so that what runs last
+  // is short (a block alone on its SM does not go faster than one of three): 64 x 1 over 1000 .. 32000 behind a window of
+  // 4096 of 32/8 heads of 128 in one part 84 us, in two 80, in three 83; 40 x 2 nodes over 1000 .. 9000 90, 68, 67; 64 x 2 nodes
+  // behind a window of 1000, whose blocks are short, 56, 68, 78; 32 x 3 over 500 .. 8000 of 20 heads of 64 58, 66, 72; 64 x 5
+  // (20 rows) over 1000 .. 16000 274, 308, 314.
+  if (sel && want < 2 && kv.dim == 128 && pl.few.nt <= 2 && seen >= 4096) {
+    pl.few.cluster = 1;
+    pl.few.parts = pl.parts = 2;
+    pl.few.slots = pl.slots = (size_t)(blocks * 2 * 8 * pl.few.nt);
+    return pl;
+  }
   // Clusters come in powers of two.  Where that leaves blocks unused, parts of at least 2048 tokens are worth the
   // join kernel: five parts of 16000 tokens of 80 heads of 128 take 48 us and clusters of four 54, of 2000 tokens
   // 14.6 and 13.3.  (More blocks than fit at once never paid: 128 heads x 16000 in clusters of two, parts of
