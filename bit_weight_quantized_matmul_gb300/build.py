@@ -2,18 +2,21 @@
 compiled in parallel, then linked as a shared library with the CUDA runtime
 linked statically (the library loads without libcudart.so or libcuda.so; the
 tensor-map encoder is resolved at run time through the runtime's driver entry
-point)."""
+point).  Beside it _wq_calls.so (g++), through which wq.py makes the KV cache
+calls of torch tensors."""
 import concurrent.futures as cf
 import glob
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwq.so")
+CALLS = os.path.join(PKG, "_wq_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]
@@ -31,15 +34,30 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         [os.path.join(os.path.dirname(PKG), "include", "wq.h")]
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def build_calls():
+    """_wq_calls.so against this interpreter's and this torch's headers."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-I" + i for i in include] + [os.path.join(CSRC, "wq_calls.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib")]
+    r = subprocess.run(cmd + ["-ltorch_python", "-ltorch_cpu", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on wq_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force=False, verbose=False):
@@ -60,7 +78,9 @@ def build(force=False, verbose=False):
 
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [cc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,4 +1,5 @@
-"""ctypes binding of libwq (include/wq.h): argument marshalling only.
+"""Binding of libwq (include/wq.h), by ctypes and, for the KV cache calls of torch tensors, csrc/wq_calls.cpp: argument
+marshalling only.
 
 Every compute step runs in libwq's CUDA kernels.  Importing this module loads
 ``libwq.so`` from this package directory and raises ImportError when it is
@@ -9,7 +10,6 @@ pass raw device pointers plus the current CUDA stream.
 """
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -20,6 +20,11 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libwq.so not found at {LIB_PATH}: build it first "
                       f"(python -m bit_weight_quantized_matmul_gb300.build)")
 lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _wq_calls as _calls
+except ImportError as e:
+    raise ImportError(f"_wq_calls.so not found or not loadable in {_HERE} ({e}): build it first "
+                      f"(python -m bit_weight_quantized_matmul_gb300.build)") from e
 
 # ------------------------------------------------------------------ constants
 WQ_NF4, WQ_NVFP4, WQ_NVFP4_W4A4, WQ_Q4_0, WQ_Q8_0, WQ_Q4_1, WQ_Q5_0, WQ_FP8 = 1, 2, 3, 4, 5, 6, 7, 8
@@ -293,6 +298,7 @@ class KVCache:
                              opt(k_g), opt(v_g), opt(table), 0 if table is None else table.shape[1], pages, page_size,
                              f, heads, dim)
         self.ref = ctypes.cast(ctypes.pointer(self.c), ctypes.c_void_p)
+        self.lead = (ctypes.addressof(self.c), heads, dim, self.batch)     # what the calls are handed of it
 
 
 def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, device="cuda"):
@@ -305,27 +311,9 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
     return KVCache(fmt, codes[0], scales[0], codes[1], scales[1], table, k_g, v_g)
 
 
-_pack_heads = struct.Struct("Pqqq").pack
-_kv_append, _kv_read = lib.wq_kv_append, lib.wq_kv_read
-_attend, _attend_workspace = lib.wq_attend, lib.wq_attend_workspace_bytes
-_pack_tree = struct.Struct("PPqq").pack
-_attend_ex_workspace = lib.wq_attend_ex_workspace_bytes
-_attend_ex, _kv_append_slots, _kv_keep, _tree_mask = lib.wq_attend_ex, lib.wq_kv_append_slots, lib.wq_kv_keep, lib.wq_tree_mask
-_kv_reserve, _kv_release = lib.wq_kv_reserve, lib.wq_kv_release
-
-
-def _heads(cache, t, dtype):
-    """[batch, token, head, dim] view -> the bytes of a wq_heads (dim contiguous; other strides as they are)."""
-    sb, st, sh, sd = t.stride()
-    assert t.get_device() == cache.index and t.dtype is dtype and sd == 1
-    return _pack_heads(t.data_ptr(), sb, st, sh)
-
-
-def _index(cache, t, batch):
-    if t is None:
-        return None
-    assert t.get_device() == cache.index and t.dtype is torch.int32 and t.is_contiguous() and t.numel() == batch
-    return t.data_ptr()
+_calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+    "wq_attend", "wq_attend_ex", "wq_attend_workspace_bytes", "wq_attend_ex_workspace_bytes", "wq_kv_append", "wq_kv_append_slots",
+    "wq_kv_read", "wq_kv_reserve", "wq_kv_release", "wq_kv_keep", "wq_tree_mask")))
 
 
 def _cache_stream(cache):
@@ -341,10 +329,7 @@ def kv_append(cache, k, v, start=None, counts=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_append(cache, k, v, start, counts)
-    batch, tokens, heads, dim = k.shape
-    assert v.shape == k.shape and heads == cache.heads and dim == cache.dim and batch <= cache.batch
-    rc = _kv_append(cache.ref, _heads(cache, k, torch.bfloat16), _heads(cache, v, torch.bfloat16), batch, tokens,
-                    _index(cache, start, batch), _index(cache, counts, batch), _cache_stream(cache))
+    rc = _calls.append(*cache.lead, cache.index, _cache_stream(cache), k, v, start, counts)
     if rc:
         raise WQError("wq_kv_append", rc)
 
@@ -358,15 +343,10 @@ def kv_read(cache, tokens, start=None, counts=None, out_f32=False, batch=None, s
             return kv_read(cache, tokens, start, counts, out_f32, batch)
     if batch is None:
         batch = cache.batch if start is None and counts is None else (counts if start is None else start).numel()
-    assert batch <= cache.batch
-    dt = torch.float32 if out_f32 else torch.bfloat16
-    k = torch.empty((batch, tokens, cache.heads, cache.dim), dtype=dt, device=cache.device)
-    v = torch.empty_like(k)
-    rc = _kv_read(cache.ref, _heads(cache, k, dt), _heads(cache, v, dt), batch, tokens, _index(cache, start, batch),
-                  _index(cache, counts, batch), WQ_FLAG_OUT_F32 if out_f32 else 0, _cache_stream(cache))
-    if rc:
-        raise WQError("wq_kv_read", rc)
-    return k, v
+    got = _calls.read(*cache.lead, cache.index, _cache_stream(cache), tokens, start, counts, out_f32, batch)
+    if type(got) is int:
+        raise WQError("wq_kv_read", got)
+    return got
 
 
 def kv_append_slots(cache, k, v, slots, stream=None):
@@ -375,10 +355,7 @@ def kv_append_slots(cache, k, v, slots, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_append_slots(cache, k, v, slots)
-    tokens, heads, dim = k.shape
-    assert v.shape == k.shape and heads == cache.heads and dim == cache.dim
-    assert slots.get_device() == cache.index and slots.dtype is torch.int64 and slots.is_contiguous() and slots.numel() == tokens
-    rc = _kv_append_slots(cache.ref, _rows(cache, k), _rows(cache, v), tokens, slots.data_ptr(), _cache_stream(cache))
+    rc = _calls.append_slots(*cache.lead, cache.index, _cache_stream(cache), k, v, slots)
     if rc:
         raise WQError("wq_kv_append_slots", rc)
 
@@ -395,18 +372,10 @@ def kv_reserve(cache, free, top, lens, counts, tokens, top_out=None, out=None, s
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_reserve(cache, free, top, lens, counts, tokens, top_out, out)
-    batch, dev = _turn(cache, free, top, top_out, lens), cache.device
-    if out is None:
-        out = (torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int32, device=dev),
-               torch.empty(batch + 1, dtype=torch.int32, device=dev), torch.empty(batch, dtype=torch.int32, device=dev))
-    slots, positions, starts, granted = out
-    assert slots.get_device() == cache.index and slots.dtype is torch.int64 and slots.is_contiguous() and slots.numel() == tokens
-    rc = _kv_reserve(cache.ref, free.data_ptr(), free.numel(), top.data_ptr(), (top if top_out is None else top_out).data_ptr(),
-                     batch, lens.data_ptr(), _index(cache, counts, batch), _index(cache, granted, batch), tokens, slots.data_ptr(),
-                     _index(cache, positions, tokens), _index(cache, starts, batch + 1), _cache_stream(cache))
-    if rc:
-        raise WQError("wq_kv_reserve", rc)
-    return slots, positions, starts, granted
+    got = _calls.reserve(*cache.lead, cache.index, _cache_stream(cache), free, top, lens, counts, tokens, top_out, out)
+    if type(got) is int:
+        raise WQError("wq_kv_reserve", got)
+    return got
 
 
 def kv_release(cache, free, top, lens, keep=None, top_out=None, stream=None):
@@ -415,22 +384,9 @@ def kv_release(cache, free, top, lens, keep=None, top_out=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_release(cache, free, top, lens, keep, top_out)
-    batch = _turn(cache, free, top, top_out, lens)
-    rc = _kv_release(cache.ref, free.data_ptr(), free.numel(), top.data_ptr(), (top if top_out is None else top_out).data_ptr(),
-                     batch, lens.data_ptr(), _index(cache, keep, batch), _cache_stream(cache))
+    rc = _calls.release(*cache.lead, cache.index, _cache_stream(cache), free, top, lens, keep, top_out)
     if rc:
         raise WQError("wq_kv_release", rc)
-
-
-def _turn(cache, free, top, top_out, lens):
-    """Checks what kv_reserve and kv_release share -> the batch."""
-    batch = lens.numel()
-    assert cache.tensors[4] is not None and batch <= cache.batch, "the cache has no table, or not that many rows"
-    _index(cache, lens, batch)
-    _index(cache, free, free.numel())
-    _index(cache, top, 1)
-    _index(cache, top_out, 1)
-    return batch
 
 
 def kv_keep(cache, start, path, counts=None, stream=None):
@@ -439,10 +395,7 @@ def kv_keep(cache, start, path, counts=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_keep(cache, start, path, counts)
-    batch, n = path.shape
-    assert batch <= cache.batch
-    rc = _kv_keep(cache.ref, _index(cache, start, batch), batch, _index(cache, path, batch * n), n, _index(cache, counts, batch),
-                  _cache_stream(cache))
+    rc = _calls.keep(*cache.lead, cache.index, _cache_stream(cache), start, path, counts)
     if rc:
         raise WQError("wq_kv_keep", rc)
 
@@ -455,43 +408,16 @@ def tree_mask(parents, counts=None, window=0, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return tree_mask(parents, counts, window)
-    batch, tokens = parents.shape
     index = torch._C._cuda_getDevice()
-    assert parents.get_device() == index and parents.dtype is torch.int32 and parents.is_contiguous()
-    assert counts is None or (counts.get_device() == index and counts.dtype is torch.int32 and counts.is_contiguous() and
-                              counts.numel() == batch)
-    mask = torch.empty((batch, tokens, (tokens + 31) // 32), dtype=torch.int32, device=parents.device)
-    depth = torch.empty((batch, tokens), dtype=torch.int32, device=parents.device)
-    rc = _tree_mask(parents.data_ptr(), batch, tokens, None if counts is None else counts.data_ptr(), window, mask.data_ptr(),
-                    depth.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
-    if rc:
-        raise WQError("wq_tree_mask", rc)
-    return mask, depth
-
-
-def _rows(cache, t):
-    """[token, head, dim] view of bf16 -> the bytes of a wq_heads."""
-    st, sh, sd = t.stride()
-    assert t.get_device() == cache.index and t.dtype is torch.bfloat16 and sd == 1
-    return _pack_heads(t.data_ptr(), 0, st, sh)
-
-
-def _tree(cache, tree, batch, tokens):
-    """(mask, depth) as tree_mask gives them, or of one tree for all sequences ([1, ...]) -> the bytes of a wq_tree."""
-    mask, depth = tree
-    words = (tokens + 31) // 32
-    assert mask.get_device() == cache.index and mask.dtype is torch.int32 and mask.is_contiguous()
-    assert mask.shape[1:] == (tokens, words) and mask.shape[0] in (1, batch)
-    if depth is not None:
-        assert depth.get_device() == cache.index and depth.dtype is torch.int32 and depth.is_contiguous()
-        assert depth.shape[1:] == (tokens,) and depth.shape[0] in (1, batch)
-    return _pack_tree(mask.data_ptr(), 0 if depth is None else depth.data_ptr(), tokens * words if mask.shape[0] == batch else 0,
-                      tokens if depth is not None and depth.shape[0] == batch else 0)
+    got = _calls.tree_mask(0, 0, 0, 0, index, _stream(), parents, counts, window)
+    if type(got) is int:
+        raise WQError("wq_tree_mask", got)
+    return got
 
 
 def attend_workspace_bytes(cache, batch, tokens, q_heads, max_len=0, select=False):
     """Bytes of workspace that attend() needs; select: with sinks= or tree= too."""
-    need = _attend_ex_workspace if select else _attend_workspace
+    need = lib.wq_attend_ex_workspace_bytes if select else lib.wq_attend_workspace_bytes
     return int(need(cache.ref, batch, tokens, q_heads, max_len))
 
 
@@ -513,33 +439,12 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
         with torch.cuda.stream(stream):
             return attend(cache, q, lens, counts, causal, window, scale, max_len, out, out_f32, return_lse, workspace,
                           None, sinks, tree)
-    batch, tokens, q_heads, dim = q.shape
-    assert dim == cache.dim and batch <= cache.batch
-    dt = torch.float32 if out_f32 else torch.bfloat16
-    if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=q.device)
-    else:
-        assert out.shape == q.shape
-    lse = torch.empty((batch, tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
-    if workspace is None:
-        need = (_attend_ex_workspace if sinks or tree is not None else _attend_workspace)(cache.ref, batch, tokens, q_heads, max_len)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        assert workspace.get_device() == cache.index and workspace.dtype is torch.uint8 and workspace.is_contiguous()
-    args = (cache.ref, _heads(cache, q, torch.bfloat16), _heads(cache, out, dt), None if lse is None else lse.data_ptr(), batch,
-            tokens, q_heads, _index(cache, lens, batch), _index(cache, counts, batch), max_len,
-            dim ** -0.5 if scale is None else scale, window)
-    rest = ((WQ_FLAG_CAUSAL if causal else 0) | (WQ_FLAG_OUT_F32 if out_f32 else 0),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-            _cache_stream(cache))
-    if sinks or tree is not None:
-        rc = _attend_ex(*args, sinks, None if tree is None else _tree(cache, tree, batch, tokens), *rest)
-    else:
-        rc = _attend(*args, *rest)
-    if rc:
-        raise WQError("wq_attend", rc)
-    return (out, lse) if return_lse else out
+    mask, depth = (None, None) if tree is None else tree
+    got = _calls.attend(*cache.lead, cache.index, _cache_stream(cache), q, lens, counts, causal, window, scale, max_len, out, out_f32,
+                        return_lse, workspace, sinks, mask, depth)
+    if type(got) is int:
+        raise WQError("wq_attend", got)
+    return got
 
 
 def last_device_status():
