@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   constexpr bool kQSmem = NT > 2;       // Q fragments live in shared memory instead of registers
   extern __shared__ __align__(128) uint8_t smem[];
   const AttendArgs& a = p.a;
+  if (SEL) griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
 
   uint32_t x = blockIdx.x;
@@ -877,6 +878,13 @@ int launch(const Params& p, cudaStream_t s) {
   if (!allow_smem(allowed, attend_kernel<FMT, D, NT, SEL>, smem_bytes(D, NT))) return WQ_ERR_CUDA;
   const int64_t grid = p.a.batch * p.a.kv.heads * p.cluster * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+  if (SEL) {
+    const dim3 blocks((unsigned)grid), threads(32 * kWarps);
+    if (launch_early(attend_kernel<FMT, D, NT, SEL>, blocks, threads, smem_bytes(D, NT), s, (unsigned)p.cluster, p) != cudaSuccess)
+      return WQ_ERR_CUDA;
+    count_launch();
+    return WQ_OK;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(32 * kWarps);

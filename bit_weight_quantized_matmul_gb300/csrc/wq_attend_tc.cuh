@@ -224,6 +224,10 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
     attend_tc_kernel(const __grid_constant__ Params p) {
   using L = Lay<D, GROUPS, SEL>;
   const AttendArgs& a = p.a;
+  if (SEL) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -714,7 +718,12 @@ int launch(const Params& p, cudaStream_t s) {
   if (!allow_smem(allowed, attend_tc_kernel<FMT, D, GROUPS, SEL>, L::TOTAL)) return WQ_ERR_CUDA;
   const int64_t grid = p.a.batch * p.a.kv.heads * p.row_tiles * p.parts;
   if (grid > 0x7FFFFFFF) return WQ_ERR_SHAPE;
-  attend_tc_kernel<FMT, D, GROUPS, SEL><<<(unsigned)grid, L::THREADS, L::TOTAL, s>>>(p);
+  if (SEL) {
+    if (launch_early(attend_tc_kernel<FMT, D, GROUPS, SEL>, dim3((unsigned)grid), dim3(L::THREADS), L::TOTAL, s, 1u, p) != cudaSuccess)
+      return WQ_ERR_CUDA;
+  } else {
+    attend_tc_kernel<FMT, D, GROUPS, SEL><<<(unsigned)grid, L::THREADS, L::TOTAL, s>>>(p);
+  }
   count_launch();
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }

@@ -46,6 +46,28 @@ inline bool allow_smem(std::atomic<uint64_t>& done, Kernel* kern, int bytes) {
   });
 }
 
+// Launches `kernel` so that it may begin while the kernel before it on the stream ends: the launch is then not waited for,
+// which is a microsecond of a call of few tokens.  The kernel calls griddep_wait() before it touches memory, and lets the next one
+// begin (griddep_launch_dependents()) only behind that: then what came before it is complete for the next one too.
+template <class... Params, class... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 blocks, dim3 threads, size_t smem, cudaStream_t s, unsigned cluster,
+                                const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = blocks;
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- pack / dequant / activation quantiser (wq_pack.cu)
 int pack_nf4(const float* W, int64_t N, int64_t K, uint8_t* packed, uint8_t* scales, cudaStream_t s);
 int pack_nvfp4(const float* W, int64_t N, int64_t K, uint8_t* packed, uint8_t* scales, cudaStream_t s);

@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_slots_kernel(const __grid_constant__ KvSlotArgs a, const int wide) {
   constexpr int kPer = D / 8;
+  griddep_wait();
+  griddep_launch_dependents();
   const int which = blockIdx.y, rounds = (a.kv.heads + kAppendRounds - 1) / kAppendRounds;
   const int chunk = blockIdx.x / (unsigned)rounds, h0 = (blockIdx.x - chunk * rounds) * kAppendRounds;
   const int tok = threadIdx.x / kPer, e = (threadIdx.x % kPer) * 8, heads = min(kAppendRounds, a.kv.heads - h0);
@@ -423,7 +425,8 @@ int append_slots_t(const KvSlotArgs& a, cudaStream_t s) {
   const int wide = (int)(a.tokens < kThreads / kPer ? a.tokens : kThreads / kPer);
   const int64_t blocks = (a.tokens + wide - 1) / wide * ((a.kv.heads + kAppendRounds - 1) / kAppendRounds);
   if (blocks > 0x7FFFFFFF) return WQ_ERR_SHAPE;
-  kv_append_slots_kernel<FMT, D><<<dim3((unsigned)blocks, 2), (wide * kPer + 31) / 32 * 32, 0, s>>>(a, wide);
+  if (launch_early(kv_append_slots_kernel<FMT, D>, dim3((unsigned)blocks, 2), dim3((wide * kPer + 31) / 32 * 32), 0, s, 1u, a, wide) != cudaSuccess)
+    return WQ_ERR_CUDA;
   return launched();
 }
 template <int FMT, int D, int ROUNDS>

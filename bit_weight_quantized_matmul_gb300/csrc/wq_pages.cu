@@ -80,11 +80,14 @@ __global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant
   __shared__ int32_t first_of[kMost], start_of[kMost], len_of[kMost], have_of[kMost];   // have -1: no pages for it
   __shared__ unsigned long long edge;              // pages that those before the first one without its pages take
   const KvArgs& kv = a.kv;
+  if (what & WRITE) {
+    griddep_wait();                                // what the COUNT launch reads before it waits is written by now
+    griddep_launch_dependents();
+  }
   const int64_t top = min(max((int64_t)*a.top, (int64_t)0), a.free_size);
   int32_t* table = const_cast<int32_t*>(kv.table);
   int64_t pages = 0, tokens = 0;                   // of the sequences before this round's
   const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
-  if (what & WRITE) griddep_launch_dependents();
   if (threadIdx.x == 0) edge = ~0ull;
 
   for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
@@ -168,10 +171,13 @@ __global__ void __launch_bounds__(kMost) kv_release_kernel(const __grid_constant
   __shared__ int64_t part[32][2];
   __shared__ int32_t first_of[kMost], have_of[kMost];
   const KvArgs& kv = a.kv;
+  if (what & WRITE) {
+    griddep_wait();                                // what the COUNT launch reads before it waits is written by now
+    griddep_launch_dependents();
+  }
   const int64_t top = min(max((int64_t)*a.top, (int64_t)0), a.free_size);
   const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
   int64_t pages = 0;
-  if (what & WRITE) griddep_launch_dependents();
   for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
     const int64_t b = b0 + threadIdx.x;
     int have = 0, need = 0;
@@ -212,6 +218,8 @@ __global__ void __launch_bounds__(kMost) tree_mask_kernel(const int32_t* __restr
                                                           int64_t batch, int tokens, int words, int64_t window,
                                                           uint32_t* __restrict__ mask, int32_t* __restrict__ depth) {
   __shared__ int16_t up[kMost];
+  griddep_wait();
+  griddep_launch_dependents();
   for (int64_t b = blockIdx.x; b < batch; b += gridDim.x) {
     const int n = kv::count_of(counts, b, tokens), i = threadIdx.x;
     if (i < tokens) {
@@ -246,6 +254,8 @@ __global__ void __launch_bounds__(kMost) tree_mask_kernel(const int32_t* __restr
 constexpr int kKeepThreads = 128;
 __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_constant__ KvKeepArgs a) {
   extern __shared__ __align__(16) uint8_t held[];
+  griddep_wait();
+  griddep_launch_dependents();
   const KvArgs& kv = a.kv;
   const int which = blockIdx.y, h = blockIdx.x;
   const int code_bytes = kv.dim / 2, scale_bytes = kv.dim / 16, pieces = code_bytes / 16;
@@ -277,11 +287,6 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   }
 }
 
-int launched() {
-  count_launch();
-  return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
-}
-
 // work: tokens or pages, at most.
 template <class Kernel>
 int launch_turn(Kernel* kernel, const KvReserveArgs& a, int64_t work, cudaStream_t s) {
@@ -289,20 +294,12 @@ int launch_turn(Kernel* kernel, const KvReserveArgs& a, int64_t work, cudaStream
   const int blocks = want > kSms ? kSms : want < 1 ? 1 : (int)want;
   const int threads = blocks > 1 || wide > kMost ? kMost : wide < 128 ? 128 : (int)wide;
   const bool once = blocks == 1 || a.top_out != a.top;
-  kernel<<<blocks, threads, 0, s>>>(a, once ? WRITE | COUNT : WRITE);
-  int rc = launched();
-  if (rc != WQ_OK || once) return rc;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a, (int)COUNT) != cudaSuccess) return WQ_ERR_CUDA;
-  return launched();
+  if (launch_early(kernel, dim3(blocks), dim3(threads), 0, s, 1u, a, once ? WRITE | COUNT : WRITE) != cudaSuccess) return WQ_ERR_CUDA;
+  count_launch();
+  if (once) return WQ_OK;
+  if (launch_early(kernel, dim3(1), dim3(threads), 0, s, 1u, a, COUNT) != cudaSuccess) return WQ_ERR_CUDA;
+  count_launch();
+  return WQ_OK;
 }
 
 }  // namespace
@@ -313,15 +310,19 @@ int kv_release(const KvReserveArgs& a, cudaStream_t s) { return launch_turn(kv_r
 int tree_mask(const int32_t* parents, const int32_t* counts, int64_t batch, int64_t tokens, int64_t window, uint32_t* mask,
               int32_t* depth, cudaStream_t s) {
   const unsigned threads = (unsigned)((tokens + 31) / 32 * 32), blocks = (unsigned)(batch < 65535 ? batch : 65535);
-  tree_mask_kernel<<<blocks, threads, 0, s>>>(parents, counts, batch, (int)tokens, (int)((tokens + 31) / 32), window, mask, depth);
-  return launched();
+  if (launch_early(tree_mask_kernel, dim3(blocks), dim3(threads), 0, s, 1u, parents, counts, batch, tokens, (tokens + 31) / 32, window, mask,
+                   depth) != cudaSuccess)
+    return WQ_ERR_CUDA;
+  count_launch();
+  return WQ_OK;
 }
 
 int kv_keep(const KvKeepArgs& a, cudaStream_t s) {
   const dim3 blocks((unsigned)a.kv.heads, 2, (unsigned)(a.batch < 65535 ? a.batch : 65535));
   const size_t smem = (size_t)a.path_ld * (a.kv.dim / 2 + a.kv.dim / 16);
-  kv_keep_kernel<<<blocks, kKeepThreads, smem, s>>>(a);
-  return launched();
+  if (launch_early(kv_keep_kernel, blocks, dim3(kKeepThreads), smem, s, 1u, a) != cudaSuccess) return WQ_ERR_CUDA;
+  count_launch();
+  return WQ_OK;
 }
 
 int take_status_pages() {
