@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   auto sees = [&](int j, int c, int t0) {
     const int r = 8 * j + 2 * q + c;
     const uint32_t* nodes = tree && r < rows ? a.tree_mask + b * a.mask_batch + (int64_t)(r / p.group) * a.tree_words : nullptr;
-    return kv::sight(t0, c_lo[j][c], c_hi[j][c], a.window ? a.sinks : 0, nodes, a.tree_words, base, held);
+    return kv::sight<false>(t0, c_lo[j][c], c_hi[j][c], a.window ? a.sinks : 0, nodes, a.tree_words, base, held);
   };
 
   float o[NT][2 * NB][4], m[NT][2], l[NT][2];

@@ -396,8 +396,14 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
         }
         const bool masked = __any_sync(0xFFFFFFFFu, (t0 < lo && !(SEL && t0 + kTile <= sinks)) || t0 + kTile > hi || (odd & 1u));
         // what this row sees of the 32 tokens from c on, as bits
+        // SEL: looked up once for both passes where two blocks share the registers, which then hold fewer addresses (26 nodes
+        // over 60001 63 -> 59 us; with one block an SM, 20 to 64 nodes, 271 -> 277).
+        constexpr bool kOnce = SEL && L::BLOCKS == 2;
+        auto bits = [&](int c) { return kv::sight<!kOnce>(t0 + c, lo, hi, sinks, nodes, a.tree_words, base, held) & ~marks[c >> 5].x; };
+        const uint4 seen = kOnce && masked ? make_uint4(bits(0), bits(32), bits(64), bits(96)) : make_uint4(0, 0, 0, 0);
         auto sees = [&](int c) -> uint32_t {
-          if (SEL) return kv::sight(t0 + c, lo, hi, sinks, nodes, a.tree_words, base, held) & ~marks[c >> 5].x;
+          if (kOnce) return c < 64 ? (c < 32 ? seen.x : seen.y) : c < 96 ? seen.z : seen.w;
+          if (SEL) return bits(c);
           const int first = lo - (t0 + c), past = hi - (t0 + c);
           uint32_t bits = past >= 32 ? 0xFFFFFFFFu : past <= 0 ? 0u : (1u << past) - 1u;
           if (first > 0) bits = first >= 32 ? 0u : bits & ~((1u << first) - 1u);

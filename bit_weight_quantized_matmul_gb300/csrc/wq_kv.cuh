@@ -108,14 +108,15 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t b) {
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 // Of the 32 tokens from t0 on: those in [lo, hi), the first `sinks` below hi, and, where bits of drafted nodes are given
 // (`words` of them), of the positions base + j below `end` those whose bit j is set.  hi is at most base then.
+// JUMP: a branch around the nodes, else none, so that the loads of several calls are under way together.
+template <bool JUMP>
 __device__ __forceinline__ uint32_t sight(int t0, int lo, int hi, int sinks, const uint32_t* nodes, int words, int base, int end) {
-  uint32_t see = (bits_below(hi - t0) & ~bits_below(lo - t0)) | bits_below(min(sinks, hi) - t0);
-  if (nodes && end > t0 && base < t0 + 32) {
-    const int at = t0 - base, w = at >> 5;               // bit of t0, -31 or more
-    const uint32_t a = w >= 0 && w < words ? nodes[w] : 0u, b = w + 1 < words ? nodes[w + 1] : 0u;
-    see |= __funnelshift_r(a, b, at & 31) & bits_below(end - t0);
-  }
-  return see;
+  const uint32_t see = (bits_below(hi - t0) & ~bits_below(lo - t0)) | bits_below(min(sinks, hi) - t0);
+  const bool some = nodes && end > t0 && base < t0 + 32;
+  if (JUMP && !some) return see;
+  const int at = some ? t0 - base : 0, w = at >> 5;      // bit of t0, -31 or more
+  const uint32_t a = some && w >= 0 && w < words ? nodes[w] : 0u, b = some && w + 1 < words ? nodes[w + 1] : 0u;
+  return see | (__funnelshift_r(a, b, at & 31) & (some ? bits_below(end - t0) : 0u));
 }
 
 // Which sequence sees the rank'th most tokens (of equals the lower number first): where there are more blocks than places, those
