@@ -86,6 +86,18 @@ int32_t* ints(const Where& w, PyObject* o, int64_t n) { return values<int32_t>(w
 at::TensorOptions on(const Where& w, at::ScalarType type) {
   return at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(w.device));
 }
+// Outputs that are made together lie in one allocation (each of them costs as much as the launch): a contiguous tensor over the
+// part of `whole` (bytes) that begins at `from`, which moves behind it, to a multiple of 16.
+at::Tensor part(const at::Tensor& whole, int64_t& from, at::ScalarType type, at::IntArrayRef sizes) {
+  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), meta);
+  t.unsafeGetTensorImpl()->set_storage_offset(from / static_cast<int64_t>(meta.itemsize()));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  from += (t.numel() * static_cast<int64_t>(meta.itemsize()) + 15) / 16 * 16;
+  return t;
+}
+at::Tensor bytes_on(const Where& w, int64_t n) { return at::empty({n}, on(w, at::kByte)); }
+
 PyObject* done(int rc) {
   if (rc != WQ_OK) return PyLong_FromLong(rc);
   Py_RETURN_NONE;
@@ -107,8 +119,14 @@ PyObject* attend(const Where& w, PyObject* const* a) {
   const bool tree = a[12] != Py_None;
   const int64_t sinks = integer(a[11]), window = integer(a[4]), max_len = integer(a[6]);
   const bool sel = tree || sinks != 0;
-  at::Tensor out;
-  if (a[7] == Py_None) {
+  const bool wants_lse = truth(a[9]);
+  at::Tensor out, lse;
+  if (a[7] == Py_None && wants_lse) {
+    int64_t from = 0;
+    const at::Tensor whole = bytes_on(w, q.numel() * (type == at::kFloat ? 4 : 2) + 16 + batch * tokens * q_heads * 4);
+    out = part(whole, from, type, q.sizes());
+    lse = part(whole, from, at::kFloat, {batch, tokens, q_heads});
+  } else if (a[7] == Py_None) {
     out = at::empty(q.sizes(), on(w, type));
   } else {
     out = tensor(a[7]);
@@ -141,8 +159,8 @@ PyObject* attend(const Where& w, PyObject* const* a) {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     scale = static_cast<float>(v);
   }
-  at::Tensor lse, workspace;
-  if (truth(a[9])) lse = at::empty({batch, tokens, q_heads}, on(w, at::kFloat));
+  at::Tensor workspace;
+  if (wants_lse && !lse.defined()) lse = at::empty({batch, tokens, q_heads}, on(w, at::kFloat));
   if (a[10] == Py_None) {
     const size_t need = (sel ? lib.ex_workspace : lib.workspace)(w.cache, batch, tokens, q_heads, max_len);
     if (need) workspace = at::empty({static_cast<int64_t>(need)}, on(w, at::kByte));
@@ -220,8 +238,11 @@ PyObject* reserve(const Where& w, PyObject* const* a) {
   const int32_t* counts = ints(w, a[3], t.batch);
   PyObject* out = a[6];
   if (out == Py_None) {
-    const at::Tensor made[4] = {at::empty({tokens}, on(w, at::kLong)), at::empty({tokens}, on(w, at::kInt)),
-                                at::empty({t.batch + 1}, on(w, at::kInt)), at::empty({t.batch}, on(w, at::kInt))};
+    want(tokens >= 0, "tokens is negative");
+    int64_t from = 0;
+    const at::Tensor whole = bytes_on(w, 12 * tokens + 8 * t.batch + 4 * 16);
+    const at::Tensor made[4] = {part(whole, from, at::kLong, {tokens}), part(whole, from, at::kInt, {tokens}),
+                                part(whole, from, at::kInt, {t.batch + 1}), part(whole, from, at::kInt, {t.batch})};
     out = PyTuple_New(4);
     if (!out) throw python_error();
     for (int i = 0; i < 4; ++i) {
@@ -265,7 +286,10 @@ PyObject* tree_mask(const Where& w, PyObject* const* a) {
   want(parents.dim() == 2, "parents is [batch, tokens]");
   const int64_t batch = parents.size(0), tokens = parents.size(1), window = integer(a[2]);
   const int32_t *up = ints(w, a[0], parents.numel()), *counts = ints(w, a[1], batch);
-  const at::Tensor mask = at::empty({batch, tokens, (tokens + 31) / 32}, on(w, at::kInt)), depth = at::empty({batch, tokens}, on(w, at::kInt));
+  const int64_t words = (tokens + 31) / 32;
+  int64_t from = 0;
+  const at::Tensor whole = bytes_on(w, batch * tokens * (words + 1) * 4 + 2 * 16);
+  const at::Tensor mask = part(whole, from, at::kInt, {batch, tokens, words}), depth = part(whole, from, at::kInt, {batch, tokens});
   const int rc = lib.tree_mask(up, batch, tokens, counts, window, static_cast<uint32_t*>(mask.data_ptr()), static_cast<int32_t*>(depth.data_ptr()),
                                w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : pair(mask, depth);
