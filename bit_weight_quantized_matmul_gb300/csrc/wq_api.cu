@@ -463,7 +463,7 @@ int wq_kv_reserve(const wq_kv_cache* cache, const int32_t* free_pages, int64_t f
   KvReserveArgs a{};
   const int rc = check_turn(cache, free_pages, free_size, top, top_out, batch, lens, a);
   if (rc != WQ_OK) return rc;
-  if (tokens < 0 || (batch > 0 && !counts) || (granted && granted == counts)) return WQ_ERR_ARG;
+  if (tokens < 0 || (batch > 0 && !counts) || (granted && (granted == counts || granted == lens))) return WQ_ERR_ARG;
   if (tokens > 0x7FFFFFFF) return WQ_ERR_SHAPE;
   if (!aligned(counts, 4) || !aligned(granted, 4) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(starts, 4))
     return WQ_ERR_ALIGN;

@@ -38,6 +38,12 @@ struct Where {
 };
 constexpr int kLead = 6;
 
+// Other threads of the interpreter run while memory is allocated or a launch waits for room in its queue.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 struct Refused {
   const char* what;
 };
@@ -96,7 +102,17 @@ at::Tensor part(const at::Tensor& whole, int64_t& from, at::ScalarType type, at:
   from += (t.numel() * static_cast<int64_t>(meta.itemsize()) + 15) / 16 * 16;
   return t;
 }
-at::Tensor bytes_on(const Where& w, int64_t n) { return at::empty({n}, on(w, at::kByte)); }
+at::Tensor empty(at::IntArrayRef sizes, const Where& w, at::ScalarType type) {
+  const Unlocked unlocked;
+  return at::empty(sizes, on(w, type));
+}
+at::Tensor bytes_on(const Where& w, int64_t n) { return empty({n}, w, at::kByte); }
+// A function of libwq.
+template <class F, class... Args>
+auto run(F* f, Args... args) {
+  const Unlocked unlocked;
+  return f(args...);
+}
 
 PyObject* done(int rc) {
   if (rc != WQ_OK) return PyLong_FromLong(rc);
@@ -127,7 +143,7 @@ PyObject* attend(const Where& w, PyObject* const* a) {
     out = part(whole, from, type, q.sizes());
     lse = part(whole, from, at::kFloat, {batch, tokens, q_heads});
   } else if (a[7] == Py_None) {
-    out = at::empty(q.sizes(), on(w, type));
+    out = empty(q.sizes(), w, type);
   } else {
     out = tensor(a[7]);
     want(out.sizes() == q.sizes(), "out has another shape than q");
@@ -160,10 +176,10 @@ PyObject* attend(const Where& w, PyObject* const* a) {
     scale = static_cast<float>(v);
   }
   at::Tensor workspace;
-  if (wants_lse && !lse.defined()) lse = at::empty({batch, tokens, q_heads}, on(w, at::kFloat));
+  if (wants_lse && !lse.defined()) lse = empty({batch, tokens, q_heads}, w, at::kFloat);
   if (a[10] == Py_None) {
     const size_t need = (sel ? lib.ex_workspace : lib.workspace)(w.cache, batch, tokens, q_heads, max_len);
-    if (need) workspace = at::empty({static_cast<int64_t>(need)}, on(w, at::kByte));
+    if (need) workspace = empty({static_cast<int64_t>(need)}, w, at::kByte);
   } else {
     workspace = tensor(a[10]);
     placed(w, workspace, at::kByte);
@@ -173,9 +189,9 @@ PyObject* attend(const Where& w, PyObject* const* a) {
   void* work = workspace.defined() ? workspace.data_ptr() : nullptr;
   const size_t bytes = workspace.defined() ? workspace.numel() : 0;
   const unsigned flags = (truth(a[3]) ? WQ_FLAG_CAUSAL : 0u) | (type == at::kFloat ? WQ_FLAG_OUT_F32 : 0u);
-  const int rc = sel ? lib.attend_ex(w.cache, &qh, &oh, lse_at, batch, tokens, q_heads, lens, counts, max_len, scale, window, sinks,
+  const int rc = sel ? run(lib.attend_ex, w.cache, &qh, &oh, lse_at, batch, tokens, q_heads, lens, counts, max_len, scale, window, sinks,
                                      tree ? &t : nullptr, flags, work, bytes, w.stream)
-                     : lib.attend(w.cache, &qh, &oh, lse_at, batch, tokens, q_heads, lens, counts, max_len, scale, window, flags, work,
+                     : run(lib.attend, w.cache, &qh, &oh, lse_at, batch, tokens, q_heads, lens, counts, max_len, scale, window, flags, work,
                                   bytes, w.stream);
   if (rc != WQ_OK) return PyLong_FromLong(rc);
   if (lse.defined()) return pair(out, lse);
@@ -188,7 +204,7 @@ PyObject* append(const Where& w, PyObject* const* a) {
   want(k.dim() == 4 && v.sizes() == k.sizes() && k.size(2) == w.heads && k.size(3) == w.dim && k.size(0) <= w.batch,
        "k and v are [batch, tokens, heads, dim], of the cache's heads and at most its sequences");
   const wq_heads kh = heads_of(w, k, at::kBFloat16), vh = heads_of(w, v, at::kBFloat16);
-  return done(lib.append(w.cache, &kh, &vh, k.size(0), k.size(1), ints(w, a[2], k.size(0)), ints(w, a[3], k.size(0)), w.stream));
+  return done(run(lib.append, w.cache, &kh, &vh, k.size(0), k.size(1), ints(w, a[2], k.size(0)), ints(w, a[3], k.size(0)), w.stream));
 }
 
 // (k, v, slots)
@@ -200,7 +216,7 @@ PyObject* append_slots(const Where& w, PyObject* const* a) {
   want(k.stride(2) == 1 && v.stride(2) == 1, "the elements of a head are not contiguous");
   want(a[2] != Py_None, "slots are expected");
   const wq_heads kh{k.data_ptr(), 0, k.stride(0), k.stride(1)}, vh{v.data_ptr(), 0, v.stride(0), v.stride(1)};
-  return done(lib.append_slots(w.cache, &kh, &vh, k.size(0), values<int64_t>(w, a[2], k.size(0), at::kLong), w.stream));
+  return done(run(lib.append_slots, w.cache, &kh, &vh, k.size(0), values<int64_t>(w, a[2], k.size(0), at::kLong), w.stream));
 }
 
 // (tokens, start, counts, out_f32, batch)
@@ -209,9 +225,9 @@ PyObject* read(const Where& w, PyObject* const* a) {
   want(batch <= w.batch, "more sequences than the cache has");
   const at::ScalarType type = truth(a[3]) ? at::kFloat : at::kBFloat16;
   const int32_t *start = ints(w, a[1], batch), *counts = ints(w, a[2], batch);
-  const at::Tensor k = at::empty({batch, tokens, w.heads, w.dim}, on(w, type)), v = at::empty({batch, tokens, w.heads, w.dim}, on(w, type));
+  const at::Tensor k = empty({batch, tokens, w.heads, w.dim}, w, type), v = empty({batch, tokens, w.heads, w.dim}, w, type);
   const wq_heads kh = heads_of(w, k, type), vh = heads_of(w, v, type);
-  const int rc = lib.read(w.cache, &kh, &vh, batch, tokens, start, counts, type == at::kFloat ? WQ_FLAG_OUT_F32 : 0u, w.stream);
+  const int rc = run(lib.read, w.cache, &kh, &vh, batch, tokens, start, counts, type == at::kFloat ? WQ_FLAG_OUT_F32 : 0u, w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : pair(k, v);
 }
 
@@ -261,7 +277,7 @@ PyObject* reserve(const Where& w, PyObject* const* a) {
   int64_t* slots = values<int64_t>(w, PyTuple_GET_ITEM(out, 0), tokens, at::kLong);
   int32_t *positions = ints(w, PyTuple_GET_ITEM(out, 1), tokens), *starts = ints(w, PyTuple_GET_ITEM(out, 2), t.batch + 1);
   int32_t* granted = ints(w, PyTuple_GET_ITEM(out, 3), t.batch);
-  const int rc = lib.reserve(w.cache, t.free, t.size, t.top, t.top_out, t.batch, t.lens, counts, granted, tokens, slots, positions, starts,
+  const int rc = run(lib.reserve, w.cache, t.free, t.size, t.top, t.top_out, t.batch, t.lens, counts, granted, tokens, slots, positions, starts,
                              w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : held.release();
 }
@@ -269,7 +285,7 @@ PyObject* reserve(const Where& w, PyObject* const* a) {
 // (free, top, lens, keep, top_out)
 PyObject* release(const Where& w, PyObject* const* a) {
   const Turn t = turn(w, a[0], a[1], a[2], a[4]);
-  return done(lib.release(w.cache, t.free, t.size, t.top, t.top_out, t.batch, t.lens, ints(w, a[3], t.batch), w.stream));
+  return done(run(lib.release, w.cache, t.free, t.size, t.top, t.top_out, t.batch, t.lens, ints(w, a[3], t.batch), w.stream));
 }
 
 // (start, path, counts)
@@ -277,7 +293,7 @@ PyObject* keep(const Where& w, PyObject* const* a) {
   const at::Tensor& path = tensor(a[1]);
   want(path.dim() == 2 && path.size(0) <= w.batch, "path is [batch, n], of at most the cache's sequences");
   const int64_t batch = path.size(0);
-  return done(lib.keep(w.cache, ints(w, a[0], batch), batch, ints(w, a[1], path.numel()), path.size(1), ints(w, a[2], batch), w.stream));
+  return done(run(lib.keep, w.cache, ints(w, a[0], batch), batch, ints(w, a[1], path.numel()), path.size(1), ints(w, a[2], batch), w.stream));
 }
 
 // (parents, counts, window); no cache
@@ -290,7 +306,7 @@ PyObject* tree_mask(const Where& w, PyObject* const* a) {
   int64_t from = 0;
   const at::Tensor whole = bytes_on(w, batch * tokens * (words + 1) * 4 + 2 * 16);
   const at::Tensor mask = part(whole, from, at::kInt, {batch, tokens, words}), depth = part(whole, from, at::kInt, {batch, tokens});
-  const int rc = lib.tree_mask(up, batch, tokens, counts, window, static_cast<uint32_t*>(mask.data_ptr()), static_cast<int32_t*>(depth.data_ptr()),
+  const int rc = run(lib.tree_mask, up, batch, tokens, counts, window, static_cast<uint32_t*>(mask.data_ptr()), static_cast<int32_t*>(depth.data_ptr()),
                                w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : pair(mask, depth);
 }

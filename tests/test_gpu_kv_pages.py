@@ -354,3 +354,78 @@ def test_a_drafting_step(fmt):
         for j in range(2):
             assert np.array_equal(got[j][b, :len(kept[b])].cpu().numpy(), rows[2 + b][j])
     assert m.last_device_status() == 0
+
+
+# ------------------------------------------------------------------ how calls may be made
+def test_on_a_stream_that_is_given():
+    need_gpu()
+    m, case, side = wq(), Case(85, "q4_0", 2, 64, 2, 96, 16), torch.cuda.Stream()
+    cache, before = case.upload(), [a.copy() for pair in case.rows for a in pair]
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    turns, stack, top = small_cache(16, 9, table), ints([4, 7, 2, 0, 8, -1, -1, -1, -1]), ints([5])
+    k, path, parents = bf16(case.rng, 3, 2, 64).cuda(), ints([[2, 1, 4]]), ints([[-1, 0, 0]])
+    side.wait_stream(torch.cuda.current_stream())
+    got = m.kv_reserve(turns, stack, top, ints([0, 0]), ints([17, 1]), 20, stream=side)
+    m.kv_release(turns, stack, top, ints([17, 1]), ints([16, 1]), stream=side)
+    m.kv_append_slots(cache, k, k, torch.tensor([1, 40, 3], device="cuda"), stream=side)
+    m.kv_keep(cache, ints([50]), path, stream=side)
+    mask, depth = m.tree_mask(parents, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert got[0].tolist() == [8 * 16 + i for i in range(16)] + [0, 2 * 16, -1, -1] and table.tolist() == [[8, 0, -1], [2, -1, -1]]
+    assert int(top) == 3 and stack.tolist() == [4, 7, 0, 0, 8, -1, -1, -1, -1]
+    assert mask.flatten().tolist() == [1, 3, 5] and depth.tolist() == [[0, 1, 1]]
+    codes, scales = OK.encode_rows("q4_0", k.float().cpu().numpy())
+    for j in range(2):
+        for i, slot in enumerate((1, 40, 3)):
+            before[2 * j][slot // 16, :, slot % 16], before[2 * j + 1][slot // 16, :, slot % 16] = codes[i], scales[i]
+        for a in before[2 * j:2 * j + 2]:
+            (p, o), (s, t) = case.at(0, np.arange(50, 53)), case.at(0, 50 + np.array([2, 1, 4]))
+            a[p, :, o] = a[s, :, t].copy()
+    assert all(np.array_equal(raw(t), b.view(np.uint8)) for t, b in zip(case.t, before)) and m.last_device_status() == 0
+
+
+def test_empty_calls():
+    need_gpu()
+    m = wq()
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    cache, stack, top, none = small_cache(16, 9, table), ints([4, 7]), ints([2]), ints([])
+    got = m.kv_reserve(cache, stack, top, none, none, 3)
+    assert got[0].tolist() == [-1] * 3 and got[1].tolist() == [0] * 3 and got[2].tolist() == [0] and got[3].tolist() == [] and int(top) == 2
+    got = m.kv_reserve(cache, stack, top, ints([0, 3]), ints([5, 0]), 0)         # tables without slots
+    assert m.last_device_status() == 0 and got[0].numel() == 0 and got[3].tolist() == [5, 0] and int(top) == 1 and int(table[0, 0]) == 7
+    m.kv_release(cache, stack, top, none)
+    assert int(top) == 1
+    m.kv_release(cache, none, ints([0]), ints([0, 0]))
+    m.kv_keep(cache, ints([0, 0]), torch.empty((2, 0), dtype=torch.int32, device="cuda"))
+    mask, depth = m.tree_mask(torch.empty((0, 5), dtype=torch.int32, device="cuda"))
+    assert mask.shape == (0, 5, 1) and depth.shape == (0, 5) and m.last_device_status() == 0
+
+
+def test_refusals_from_python():
+    need_gpu()
+    m = wq()
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    cache, slab = small_cache(16, 9, table), small_cache(16, 9, None)
+    stack, top, two = ints([4, 7]), ints([2]), ints([0, 1])
+    launches = m.lib.wq_kernel_launches()
+    for call in (lambda: m.kv_reserve(slab, stack, top, two, two, 3), lambda: m.kv_reserve(cache, stack.cpu(), top, two, two, 3),
+                 lambda: m.kv_reserve(cache, stack, top.cpu(), two, two, 3), lambda: m.kv_reserve(cache, stack, top, two, ints([1]), 3),
+                 lambda: m.kv_reserve(cache, stack, top, ints([0] * 3), ints([0] * 3), 3), lambda: m.kv_reserve(cache, stack, None, two, two, 3),
+                 lambda: m.kv_reserve(cache, stack, top, two, two, -1), lambda: m.kv_reserve(cache, stack, top, two, two, 3, out=(two,) * 4),
+                 lambda: m.kv_reserve(cache, stack, top, two, two, 3, top_out=two), lambda: m.kv_release(slab, stack, top, two),
+                 lambda: m.kv_release(cache, stack, top, two, ints([1])), lambda: m.kv_release(cache, stack.long(), top, two),
+                 lambda: m.kv_keep(cache, two, ints([0, 1])), lambda: m.kv_keep(cache, ints([0]), ints([[0, 1], [1, 0]])),
+                 lambda: m.kv_keep(cache, ints([0] * 3), ints([[0], [1], [2]])),
+                 lambda: m.kv_append_slots(cache, torch.zeros(2, 1, 64, device="cuda"), torch.zeros(2, 1, 64, device="cuda"), two.long()),
+                 lambda: m.kv_append_slots(cache, torch.zeros(2, 1, 64, device="cuda").bfloat16(), torch.zeros(2, 1, 64, device="cuda").bfloat16(), two),
+                 lambda: m.kv_append_slots(cache, torch.zeros(2, 2, 64, device="cuda").bfloat16(), torch.zeros(2, 2, 64, device="cuda").bfloat16(),
+                                           two.long())):
+        with pytest.raises(AssertionError):
+            call()
+    with pytest.raises(m.WQError):
+        m.kv_keep(cache, ints([0]), torch.zeros((1, 513), dtype=torch.int32, device="cuda"))
+    with pytest.raises(m.WQError):
+        m.kv_reserve(cache, stack, top, two, two, 0, out=(torch.empty(0, dtype=torch.int64, device="cuda"), ints([]), ints([0] * 3), two))
+    with pytest.raises(m.WQError):
+        m.tree_mask(torch.full((1, 1025), -1, dtype=torch.int32, device="cuda"))
+    assert m.lib.wq_kernel_launches() == launches and m.last_device_status() == 0

@@ -290,3 +290,157 @@ def test_offsets_past_32_bits():
         ref, *_ = OK.attend_seen(q[0].float().numpy(), rows, rows, OK.visible(tokens, tokens, 400, 100, 5, nodes, depth), D ** -0.5)
         assert rel_l2(out[0].cpu().numpy(), ref) <= F32_REL_L2
     assert m.last_device_status() == 0
+
+
+# ------------------------------------------------------------------ more blocks than places, and what the plans do with them
+class Shared(Case):
+    """`batch` sequences over the same pages, in orders of their own (only read)."""
+
+    def __init__(self, seed, fmt, heads, D, batch, capacity, page):
+        super().__init__(seed, fmt, heads, D, 1, capacity, page)
+        self.batch, per = batch, self.table.shape[1]
+        self.table = np.stack([self.rng.permutation(self.pages)[:per] for _ in range(batch)]).astype(np.int32)
+
+
+@FMTS
+@pytest.mark.parametrize("batch", [255, 256, 257])
+def test_as_many_sequences_as_are_sorted_and_one_more(fmt, batch):
+    need_gpu()
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 130, batch)]
+    check(Shared(90, fmt, 2, 64, batch, 160, 16), 1, 2, lens, window=50, sinks=3)
+    lens[7] = lens[100] = 160
+    check(Shared(91, fmt, 2, 64, batch, 160, 16), 1, 4, lens, [int(x) for x in rng.integers(0, 2, batch)], window=70, sinks=20)
+
+
+@FMTS
+@pytest.mark.parametrize("batch,tokens,hq,h,D", [(80, 40, 8, 4, 64), (45, 40, 16, 4, 128), (160, 9, 8, 2, 128)])
+def test_many_trees_of_many_rows(fmt, batch, tokens, hq, h, D):
+    """One and two groups of rows a block, sequences of few nodes among those of many."""
+    need_gpu()
+    case = Shared(92, fmt, h, D, batch, 300, 32)
+    nodes, depth = zip(*(OK.ancestors(p, tokens) for p in random_trees(case.rng, batch, tokens)))
+    lens = [int(x) for x in case.rng.integers(tokens, 300, batch)]
+    counts = [int(x) for x in case.rng.integers(0, tokens + 1, batch)]
+    check(case, tokens, hq, lens, counts, nodes=np.stack(nodes), depth=np.stack(depth))
+    check(case, tokens, hq, lens, counts, window=60, sinks=9, nodes=np.stack(nodes))
+
+
+@FMTS
+@pytest.mark.parametrize("tokens,hq,h", [(1, 16, 4), (2, 8, 4), (4, 8, 2)])
+def test_long_sequences_in_two_parts(fmt, tokens, hq, h):
+    """More items than half of the places, and a cache for more than 4096 tokens a sequence: parts that some sequences fill
+    and others leave empty."""
+    need_gpu()
+    batch = 116 if h == 2 else 58
+    case = Shared(93, fmt, h, 128, batch, 4300, 64)
+    lens = [int(x) for x in case.rng.integers(tokens, 90, batch)]
+    lens[3], lens[20], lens[21] = 4300, 4177, 0
+    check(case, tokens, hq, lens, window=4200, sinks=5)
+    nodes, depth = zip(*(OK.ancestors(p, tokens) for p in random_trees(case.rng, batch, tokens)))
+    lens[21] = tokens
+    check(case, tokens, hq, lens, nodes=np.stack(nodes), depth=np.stack(depth))
+
+
+@FMTS
+@pytest.mark.parametrize("D,heads,batch,tokens,q_heads", [(64, 1, 1, 1, 1), (128, 2, 1, 3, 8), (64, 38, 4, 1, 38), (128, 1, 3, 20, 1), (128, 2, 1, 40, 4),
+                                                          (64, 1, 2, 150, 2), (128, 4, 60, 1, 8), (128, 2, 40, 70, 2)])
+def test_nothing_is_written_past_the_workspace(fmt, D, heads, batch, tokens, q_heads):
+    """attend_workspace_bytes(select=True) is enough for every window, number of sinks and tree."""
+    need_gpu()
+    m, n = wq(), 6400
+    case = Shared(94, fmt, heads, D, batch, n, 64)
+    cache, q = case.upload(), bf16(case.rng, batch, tokens, q_heads, D).cuda()
+    lens = ints([n - 17 * b for b in range(batch)])
+    nodes, depth = OK.ancestors(random_trees(case.rng, 1, tokens)[0], tokens)
+    tree = (cuda(OK.mask_words(nodes[None])), cuda(depth[None]))
+    need = m.attend_workspace_bytes(cache, batch, tokens, q_heads, select=True)
+    assert need >= m.attend_workspace_bytes(cache, batch, tokens, q_heads)
+    guarded = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    for window, sinks, t in ((0, 0, tree), (1, 1, None), (300, 5000, None), (1500, 4, tree), (4000, 100, None), (4095, 1, None), (5000, 64, tree),
+                             (10 ** 9, 3, None)):
+        args = dict(window=window, sinks=sinks, tree=t)
+        want = m.attend(cache, q, lens, **args)
+        got = m.attend(cache, q, lens, workspace=guarded[4096:4096 + need], **args)
+        assert torch.equal(got, want)
+        assert (guarded[:4096] == 0xA5).all() and (guarded[4096 + need:] == 0xA5).all()
+    assert m.last_device_status() == 0
+
+
+# ------------------------------------------------------------------ what buffers may hold, and how calls may be made
+@FMTS
+@pytest.mark.parametrize("tokens", [5, 40])
+def test_depths_of_any_value(fmt, tokens):
+    """Depths outside the draft are clamped to it."""
+    need_gpu()
+    case = Case(95, fmt, 2, 64, 2, 300, 16)
+    nodes, _ = zip(*(OK.ancestors(p, tokens) for p in random_trees(case.rng, 2, tokens)))
+    depth = case.rng.integers(-3, tokens + 5, (2, tokens)).astype(np.int64)
+    depth[:, 1], depth[:, 3] = 2 ** 31 - 1, -2 ** 31
+    check(case, tokens, 4, [300, 100], window=37, sinks=2, nodes=np.stack(nodes), depth=depth)
+
+
+def test_lengths_of_any_value():
+    """Lengths up to 2^31 - 1 and below zero from old buffers: reported or empty, and nothing else."""
+    need_gpu()
+    m, case = wq(), Case(96, "q4_0", 1, 64, 3, 96, 16)
+    cache = case.upload()
+    for tokens in (1, 40):
+        q = bf16(case.rng, 3, tokens, 1, 64).cuda()
+        tree = m.tree_mask(cuda(random_trees(case.rng, 3, tokens)))
+        assert m.last_device_status() == 0
+        for args in (dict(window=20, sinks=90), dict(tree=tree), dict(tree=tree, window=30, sinks=7)):
+            out, lse = m.attend(cache, q, ints([2 ** 31 - 1, -5, 96]), return_lse=True, **args)
+            assert m.last_device_status() == m.WQ_ERR_ARG
+            assert not out[1].any() and (lse[1] == -float("inf")).all()
+            alone, alse = m.attend(cache, q, ints([0, 0, 96]), return_lse=True, **args)
+            assert torch.equal(out[2], alone[2]) and torch.equal(lse[2], alse[2]) and m.last_device_status() == 0
+            assert torch.isfinite(out[0]).all()
+
+
+def test_strided_views_and_other_streams():
+    """q a column range of a wider buffer, out a view, the call on a stream given by stream=."""
+    need_gpu()
+    m, case = wq(), Case(97, "nvfp4", 2, 128, 2, 200, 32)
+    cache, lens = case.upload(), ints([200, 133])
+    side = torch.cuda.Stream()
+    for tokens in (3, 60):
+        wide = bf16(case.rng, 2, tokens, 14 * 128).cuda()
+        q = wide[..., 128:9 * 128].unflatten(-1, (8, 128))
+        tree = m.tree_mask(cuda(random_trees(case.rng, 2, tokens)))
+        args = dict(window=64, sinks=3, tree=tree)
+        want, wlse = m.attend(cache, q.contiguous(), lens, return_lse=True, **args)
+        full = torch.full((2, tokens + 2, 9, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = full[:, 1:-1, :8]
+        side.wait_stream(torch.cuda.current_stream())
+        got, lse = m.attend(cache, q, lens, out=out, return_lse=True, stream=side, **args)
+        torch.cuda.current_stream().wait_stream(side)
+        assert got.data_ptr() == out.data_ptr() and torch.equal(out, want) and torch.equal(lse, wlse)
+        assert (full[:, 0] == 7).all() and (full[:, -1] == 7).all() and (full[:, :, 8] == 7).all()
+        assert lse.is_contiguous() and lse.shape == (2, tokens, 8) and want.is_contiguous() and want.untyped_storage().data_ptr() % 16 == 0
+
+
+def test_refusals_from_python():
+    need_gpu()
+    m, case = wq(), Case(98, "q4_0", 2, 64, 2, 200, 32)
+    cache, lens, q = case.upload(), ints([200, 133]), bf16(case.rng, 2, 5, 4, 64).cuda()
+    mask, depth = m.tree_mask(cuda(random_trees(case.rng, 2, 5)))
+    launches = m.lib.wq_kernel_launches()
+    for bad in (dict(tree=(mask.cpu(), depth)), dict(tree=(mask, depth.cpu())), dict(tree=(mask[:, :4], depth)), dict(tree=(mask.long(), depth)),
+                dict(tree=(mask, depth[:, ::2])), dict(tree=(mask[:, :, None], depth)), dict(tree=(None, depth), sinks=1, window=1, out=q[:1])):
+        with pytest.raises(AssertionError):
+            m.attend(cache, q, lens, **bad)
+    for bad in (dict(sinks=-1), dict(sinks=1, causal=False), dict(tree=(mask, depth), causal=False), dict(window=-1, sinks=2)):
+        with pytest.raises(m.WQError):
+            m.attend(cache, q, lens, **bad)
+    for bad in (dict(counts=ints([1])), dict(counts=ints([1, 1]).cpu()), dict(window=-1)):
+        with pytest.raises((AssertionError, m.WQError)):
+            m.tree_mask(cuda(random_trees(case.rng, 2, 5)), **bad)
+    for bad in (torch.zeros(2, 5, device="cuda"), torch.zeros(2, 5, dtype=torch.int32), torch.zeros(5, dtype=torch.int32, device="cuda"), "parents"):
+        with pytest.raises(AssertionError):
+            m.tree_mask(bad)
+    with pytest.raises(TypeError):
+        m.attend(cache, q, lens, window="wide", sinks=1)
+    with pytest.raises(OverflowError):
+        m.attend(cache, q, lens, window=2 ** 63, sinks=1)
+    assert m.lib.wq_kernel_launches() == launches and m.last_device_status() == 0
