@@ -102,9 +102,16 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     // SMs are left, four tiles of 128 to a part at least.
     const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
     pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
-    if (half == 1) pl.tcp.groups = 1;
+    // Sinks and trees of heads of 64: one group where that is more than a block an SM, of which two fit (4 x 301 tokens behind a
+    // window of 292 of 20 heads two groups 43 us, one 26; 2 x 1024 behind 2048 109 and 100; 32 x 20 .. 64 nodes over 1000 ..
+    // 6000 250 and 176; below the bound 3 x 200 behind 4000 48 and 52).
+    if (half == 1 || (sel && kv.dim == 64 && heads * half > kSms)) pl.tcp.groups = 1;
     pl.tcp.row_tiles = (int)((half + pl.tcp.groups - 1) / pl.tcp.groups);
-    const int64_t tiles = (seen + 127) / 128, most = (tiles + 3) / 4, room = kSms * ((kv.dim == 64 || sel) && pl.tcp.groups == 1 ? 2 : 1);
+    // Behind a window a row tile sees what one of its tokens does and as many tokens more as it has, and a tile more for
+    // where they begin (512 tokens behind 100 of 32/8 heads of 128 21 us, two parts 27; 130 behind 400 of 32/4 24 and 21).
+    const int64_t wide = pl.tcp.groups * 128 / group + 1;
+    const int64_t mine = sel && window > 0 && window + sinks + wide + 128 < seen ? window + sinks + wide + 128 : seen;
+    const int64_t tiles = (mine + 127) / 128, most = (tiles + 3) / 4, room = kSms * ((kv.dim == 64 || sel) && pl.tcp.groups == 1 ? 2 : 1);
     int64_t want = room / (heads * pl.tcp.row_tiles);
     if (want > most) want = most;
     pl.tcp.parts = (int)(want > 1 ? want : 1);
