@@ -13,6 +13,7 @@ namespace {
 constexpr int kMost = 1024;      // threads of a block, and sequences of a round
 constexpr int kSms = 152;
 constexpr int kShare = 2048;     // tokens or pages a block is launched for
+constexpr int kRun = 128;        // neighbouring tokens that a warp takes
 
 __device__ __forceinline__ int pages_for(const KvArgs& kv, int tokens) {   // ceil(tokens / page_size), tokens < 2^31
   return tokens > 0 ? kv::page_of(kv, tokens - 1) + 1 : 0;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant
   }
   const int64_t top = min(max((int64_t)*a.top, (int64_t)0), a.free_size);
   int32_t* table = const_cast<int32_t*>(kv.table);
+  const int lane = threadIdx.x & 31;
   int64_t pages = 0, tokens = 0;                   // of the sequences before this round's
   const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
   if (threadIdx.x == 0) edge = ~0ull;
@@ -127,22 +129,34 @@ __global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant
         if ((uint32_t)page >= (uint64_t)kv.pages) set_status(WQ_STATUS_ARG);
         table[(b0 + i) * kv.table_ld + have_of[i] + ((int)e - first_of[i])] = page;
       }
+      // Tokens by warps, 128 neighbours at a time: mostly one sequence's, which is then looked up once.
       const int64_t stop = min(tokens + s.all_y, a.tokens);
-#pragma unroll 2
-      for (int64_t k = tokens + me; k < stop; k += all) {
-        const int i = last_at(start_of, seqs, (int)k);
-        const int pos = clamp32((int64_t)len_of[i] + ((int)k - start_of[i])), have = have_of[i];
-        if (a.slots) {
-          int64_t slot = -1;
-          if (have >= 0) {
-            const int p = kv::page_of(kv, pos);    // a new page's number is still on the stack
-            const int page = p >= have ? a.free_pages[top - 1 - ((int64_t)first_of[i] + (p - have))] : table[(b0 + i) * kv.table_ld + p];
-            if ((uint32_t)page < (uint64_t)kv.pages) slot = (int64_t)page * kv.page_size + (pos - p * kv.page_size);
-            else set_status(WQ_STATUS_ARG);
-          }
-          a.slots[k] = slot;
+      for (int64_t k0 = tokens + (me >> 5) * kRun; k0 < stop; k0 += (all >> 5) * kRun) {
+        const int i0 = last_at(start_of, seqs, (int)k0), rest = (int)min(stop - k0, (int64_t)kRun);
+        const bool one = i0 + 1 >= seqs || start_of[i0 + 1] >= (int)k0 + rest;
+        int page[kRun / 32], pos[kRun / 32];
+        uint32_t asked = 0;                        // bit r: a page was looked up
+#pragma unroll
+        for (int r = 0; r < kRun / 32; ++r) {
+          const int x = 32 * r + lane, i = one ? i0 : last_at(start_of, seqs, (int)k0 + min(x, rest - 1));
+          const int have = have_of[i];
+          pos[r] = clamp32((int64_t)len_of[i] + ((int)k0 + x - start_of[i]));
+          const bool ask = a.slots && have >= 0 && x < rest;
+          const int p = kv::page_of(kv, pos[r]);   // a new page's number is still on the stack
+          const int32_t* at = p >= have ? a.free_pages + (top - 1 - ((int64_t)first_of[i] + (p - have))) : table + (b0 + i) * kv.table_ld + p;
+          page[r] = ask ? *at : -1;
+          asked |= (ask ? 1u : 0u) << r;
         }
-        if (a.positions) a.positions[k] = pos;
+#pragma unroll
+        for (int r = 0; r < kRun / 32; ++r) {
+          const int x = 32 * r + lane;
+          if (x >= rest) break;
+          const int off = pos[r] - kv::page_of(kv, pos[r]) * kv.page_size;
+          const bool good = (uint32_t)page[r] < (uint64_t)kv.pages;
+          if (!good && ((asked >> r) & 1u)) set_status(WQ_STATUS_ARG);
+          if (a.slots) a.slots[k0 + x] = good ? (int64_t)page[r] * kv.page_size + off : -1;
+          if (a.positions) a.positions[k0 + x] = pos[r];
+        }
       }
       __syncthreads();
     }
