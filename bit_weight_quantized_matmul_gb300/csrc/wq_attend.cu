@@ -94,7 +94,7 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
   // are more tiles than `most` asks for, so a window that lowers `want` below 8 leaves clusters).
   const int64_t held = max_len > 0 && max_len < kv.capacity ? max_len : kv.capacity;
   const int64_t seen = window > 0 && window + tokens + sinks < held ? window + tokens + sinks : held;
-  pl.tc = rows > kFewRows;
+  pl.tc = rows > few_rows(kv.fmt, kv.dim, sel);
   if (pl.tc) {
     // Two groups of rows a block where that leaves a block for every SM, or where there is work for long (one group, two:
     // 1024 tokens of 32/8 heads of 128 over 4096 137 and 84 us, 512 of 20/20 of 64 over 8192 68 and 60; below the bound

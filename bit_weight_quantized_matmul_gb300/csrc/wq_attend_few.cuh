@@ -60,6 +60,10 @@ constexpr int kSms = 152;
 //   q4_0   this    17.4  22.4  42.9  43.6  65.4  66.2 us     the other  44.2  43.5  43.9  43.9  44.5  45.4
 //   NVFP4  this    18.4  22.4  34.1  34.8  51.8  52.3        the other  39.2  39.3  40.3  40.6  41.1  42.3
 constexpr int kFewRows = 32;
+// Sinks and trees of q4_0 heads of 128, whose 32 rows spill here most, go there from 17 rows on (20 or 32 rows; this one, the
+// other: 8 x 8 nodes over 1000 .. 4000 38.3 and 34.4 us, 4 x 5 over 400 .. 900 22.3 and 19.6, 32 x 5 over 2000 .. 8000 182 and 185;
+// NVFP4 32 x 5 144 and 168, 64 x 8 over 1000 .. 16000 286 and 317; heads of 64, NVFP4, 16 x 24 over 1000 .. 4000 49 and 73).
+constexpr int few_rows(int fmt, int dim, bool sel) { return sel && dim == 128 && fmt == WQ_Q4_0 ? 16 : kFewRows; }
 // More registers a thread beat more warps: 4, 3 and 2 blocks of NT = 1 an SM read one sequence of 2^20 tokens at
 // 4.6, 5.6 and 5.3 TB/s.
 constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -902,7 +906,10 @@ int launch(const Params& p, cudaStream_t s) {
 }
 template <int FMT, int D, bool SEL>
 int launch_nt(const Params& p, int nt, cudaStream_t s) {
-  return nt == 1 ? launch<FMT, D, 1, SEL>(p, s) : nt == 2 ? launch<FMT, D, 2, SEL>(p, s) : launch<FMT, D, 4, SEL>(p, s);
+  if constexpr (few_rows(FMT, D, SEL) > 16) {
+    if (nt == 4) return launch<FMT, D, 4, SEL>(p, s);
+  }
+  return nt == 1 ? launch<FMT, D, 1, SEL>(p, s) : launch<FMT, D, 2, SEL>(p, s);
 }
 template <bool SEL>
 int launch_few(const AttendArgs& a, const AttendFewPlan& pl, cudaStream_t s) {

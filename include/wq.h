@@ -422,6 +422,7 @@ int wq_attend(const wq_kv_cache* cache, const wq_heads* q, const wq_heads* out, 
  *                 t < lens[b] - counts[b], with a window and sinks as a token at lens[b] - counts[b] + depth[i]
  *                 (clamped to 0 .. counts[b] - 1) does, and node j, at t = lens[b] - counts[b] + j, where bit j of its
  *                 mask is set: itself too only then.  tokens <= WQ_TREE_MAX.
+ * What wq_attend says of more than 32 query rows per cached head holds from 17 on here for WQ_Q4_0 heads of 128.
  * workspace: wq_attend_ex_workspace_bytes(...) bytes, enough with and without sinks and trees; as above.   */
 size_t wq_attend_ex_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,
                                     int64_t max_len);

@@ -202,8 +202,14 @@ def test_a_chain_is_causal_attention(fmt):
             tree = m.tree_mask(parents, window=window)
             got = m.attend(cache, q, lens, window=window, tree=tree, return_lse=True, out_f32=True)
             want = m.attend(cache, q, lens, window=window, return_lse=True, out_f32=True)
-            # the same sums; tiles that one of the two masks and the other leaves out may order the running maximum otherwise
-            assert torch.allclose(got[1], want[1], rtol=0, atol=2e-5)
+            # The same sums; tiles that one of the two masks and the other leaves out may order the running maximum otherwise.
+            # q4_0 trees of 17 to 32 rows go to the kernel that rounds (c - 8) d to 11 bits, the tokens to the one that does
+            # not: each score then moves by 2^-12 of sum |scale q k| at most, and a log-sum-exp by no more than its scores.
+            off = 0.0
+            if fmt == "q4_0" and 16 < tokens * 4 <= 32:
+                off = 2.0 ** -12 * max(OK.attend_seen(q[b].float().cpu().numpy(), *case.values(b, n), np.ones((tokens, n), bool), 128 ** -0.5)[3].max()
+                                       for b, n in ((0, 400), (1, 150)))
+            assert torch.allclose(got[1], want[1], rtol=0, atol=2e-5 + off)
             assert rel_l2(got[0].cpu().numpy(), want[0].cpu().numpy()) <= F32_REL_L2
     assert m.last_device_status() == 0
 
