@@ -187,9 +187,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
   const int split = x % splits;         // the blocks of a cluster are neighbours
   x /= splits;
   const int h = x % a.kv.heads;
-  int64_t b = x / a.kv.heads;
-  if (SEL && p.sorted) b = kv::by_length<32 * kWarps>(a, (int)b, reinterpret_cast<int*>(smem));
-  const int64_t item = b * a.kv.heads + h;
+  int64_t first_b = x / a.kv.heads;
+  if constexpr (SEL) {
+    if (p.sorted) first_b = kv::by_length<32 * kWarps>(a, (int)first_b, reinterpret_cast<int*>(smem));
+  }
+  const int64_t b = first_b, item = SEL ? b * a.kv.heads + h : x;   // item: (sequence, cached head)
 
   // Q is asked for first: its addresses need nothing that is still on its way.  Lane (g, q) holds row
   // 8 j + g's elements 32 blk + 8 q .. + 7 (rows past counts[b] too: they are there, and their columns unused).
@@ -435,8 +437,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            hit[j][c] |= SEL ? (sees(j, c, t & ~31) >> (t & 31)) & 1u : t >= c_lo[j][c] && t < c_hi[j][c];
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (SEL) hit[j][c] |= ((sees(j, c, t & ~31) >> (t & 31)) & 1u) != 0;
+            else hit[j][c] |= t >= c_lo[j][c] && t < c_hi[j][c];
+          }
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -554,8 +558,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float top[2] = {-INFINITY, -INFINITY};
-      uint32_t see[2][kTile / 32];
-      if (SEL && masked) {
+      [[maybe_unused]] uint32_t see[2][kTile / 32];
+      if constexpr (SEL && masked) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -569,9 +573,12 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(NT)) attend_kernel(
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int in = 16 * u + 8 * (k >> 1) + g, t = tile * kTile + in;
-            const bool hidden = SEL ? !((see[k & 1][u >> 1] >> (in & 31)) & 1u) : t < c_lo[j][k & 1] || t >= c_hi[j][k & 1];
-            if (hidden || ((gone >> u) & 1u)) v[k] = -INFINITY;
+            const int t = tile * kTile + 16 * u + 8 * (k >> 1) + g;
+            if constexpr (SEL) {
+              if (!((see[k & 1][u >> 1] >> (t & 31)) & 1u) || ((gone >> u) & 1u)) v[k] = -INFINITY;
+            } else {
+              if (t < c_lo[j][k & 1] || t >= c_hi[j][k & 1] || ((gone >> u) & 1u)) v[k] = -INFINITY;
+            }
           }
         }
         top[0] = max3(top[0], v[0], v[2]);

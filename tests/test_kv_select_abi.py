@@ -109,3 +109,27 @@ def test_oracle_of_what_is_visible():
     q, k, v = rng.standard_normal((4, 2, 8)), rng.standard_normal((9, 1, 8)), rng.standard_normal((9, 1, 8))
     a, b = OK.attend(q, k, v, 4, 0.3, True, 5), OK.attend_seen(q, k, v, OK.visible(4, 4, 9, window=5), 0.3)
     assert all(np.allclose(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------ the binding
+def test_the_binding_refuses_host_memory_and_wrong_arguments(wq):  # noqa: F811
+    torch = pytest.importorskip("torch")
+    c = cache(wq)
+    lead = (ctypes.addressof(c), c.heads, c.dim, 2, 0, 0)
+    ints, rows, k = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, 8, 128).bfloat16(), torch.zeros(3, 8, 128).bfloat16()
+    calls = wq._calls
+    for call in (lambda: calls.attend(*lead, rows, ints, None, True, 0, None, 0, None, False, False, None, 1, None, None),
+                 lambda: calls.append(*lead, rows, rows, None, None), lambda: calls.append_slots(*lead, k, k, torch.zeros(3, dtype=torch.int64)),
+                 lambda: calls.read(*lead, 5, ints, None, False, 2), lambda: calls.reserve(*lead, ints, ints[:1], ints, ints, 5, None, None),
+                 lambda: calls.release(*lead, ints, ints[:1], ints, None, None), lambda: calls.keep(*lead, ints, torch.zeros(2, 3, dtype=torch.int32), None),
+                 lambda: calls.tree_mask(0, 0, 0, 0, 0, 0, torch.zeros(2, 3, dtype=torch.int32), None, 0),
+                 lambda: calls.attend(*lead, rows[0], ints, None, True, 0, None, 0, None, False, False, None, 1, None, None),
+                 lambda: calls.append(*lead, rows[..., :64], rows[..., :64], None, None), lambda: calls.append(*lead, "k", rows, None, None),
+                 lambda: calls.append(*lead, rows.expand(2, 3, 8, 128), rows[:1], None, None)):
+        with pytest.raises(AssertionError):
+            call()
+    for call in (lambda: calls.append(*lead, rows, rows, None), lambda: calls.tree_mask(), lambda: calls.bind(1, 2)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(TypeError):
+        calls.tree_mask(0, 0, 0, 0, 0, 0, torch.zeros(2, 3, dtype=torch.int32), None, "wide")
