@@ -135,20 +135,7 @@ PyObject* attend(const Where& w, PyObject* const* a) {
   const bool tree = a[12] != Py_None;
   const int64_t sinks = integer(a[11]), window = integer(a[4]), max_len = integer(a[6]);
   const bool sel = tree || sinks != 0;
-  const bool wants_lse = truth(a[9]);
-  at::Tensor out, lse;
-  if (a[7] == Py_None && wants_lse) {
-    int64_t from = 0;
-    const at::Tensor whole = bytes_on(w, q.numel() * (type == at::kFloat ? 4 : 2) + 16 + batch * tokens * q_heads * 4);
-    out = part(whole, from, type, q.sizes());
-    lse = part(whole, from, at::kFloat, {batch, tokens, q_heads});
-  } else if (a[7] == Py_None) {
-    out = empty(q.sizes(), w, type);
-  } else {
-    out = tensor(a[7]);
-    want(out.sizes() == q.sizes(), "out has another shape than q");
-  }
-  const wq_heads qh = heads_of(w, q, at::kBFloat16), oh = heads_of(w, out, type);
+  const wq_heads qh = heads_of(w, q, at::kBFloat16);
   const int32_t *lens = ints(w, a[1], batch), *counts = ints(w, a[2], batch);
   wq_tree t{};
   if (tree) {
@@ -175,6 +162,20 @@ PyObject* attend(const Where& w, PyObject* const* a) {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     scale = static_cast<float>(v);
   }
+  const bool wants_lse = truth(a[9]);
+  at::Tensor out, lse;
+  if (a[7] == Py_None && wants_lse) {
+    int64_t from = 0;
+    const at::Tensor whole = bytes_on(w, q.numel() * (type == at::kFloat ? 4 : 2) + 16 + batch * tokens * q_heads * 4);
+    out = part(whole, from, type, q.sizes());
+    lse = part(whole, from, at::kFloat, {batch, tokens, q_heads});
+  } else if (a[7] == Py_None) {
+    out = empty(q.sizes(), w, type);
+  } else {
+    out = tensor(a[7]);
+    want(out.sizes() == q.sizes(), "out has another shape than q");
+  }
+  const wq_heads oh = heads_of(w, out, type);
   at::Tensor workspace;
   if (wants_lse && !lse.defined()) lse = empty({batch, tokens, q_heads}, w, at::kFloat);
   if (a[10] == Py_None) {
