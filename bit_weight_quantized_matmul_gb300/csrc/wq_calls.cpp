@@ -1,7 +1,7 @@
 // wq_calls.cpp -- the KV cache calls of wq.py, from torch tensors to the C ABI: checks, outputs, the call.
 //
 // A call of few tokens costs the host more than the GPU: through ctypes, with its outputs allocated from Python, an attention
-// call took 13 us of the host's time against 8 of the GPU's, here 6.  wq.py hands over the cache (address of its wq_kv_cache, and
+// call took 13 us of the host's time against 7 of the GPU's, here 5 (a call that is given its outputs 2.5).  wq.py hands over the cache (address of its wq_kv_cache, and
 // what is checked against it), the device and the stream; a failed check raises AssertionError, a status other than WQ_OK comes
 // back as an int, which wq.py raises.  Built beside libwq.so, whose functions it gets by their addresses.
 #include <Python.h>

@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant
         uint32_t asked = 0;                        // bit r: a page was looked up
 #pragma unroll
         for (int r = 0; r < kRun / 32; ++r) {
-          const int x = 32 * r + lane, i = one ? i0 : last_at(start_of, seqs, (int)k0 + min(x, rest - 1));
+          const int k = (int)k0 + min(32 * r + lane, rest - 1), i = one ? i0 : last_at(start_of, seqs, k);
           const int have = have_of[i];
-          pos[r] = clamp32((int64_t)len_of[i] + ((int)k0 + x - start_of[i]));
-          const bool ask = a.slots && have >= 0 && x < rest;
+          pos[r] = clamp32((int64_t)len_of[i] + (k - start_of[i]));
+          const bool ask = a.slots && have >= 0 && 32 * r + lane < rest;
           const int p = kv::page_of(kv, pos[r]);   // a new page's number is still on the stack
           const int32_t* at = p >= have ? a.free_pages + (top - 1 - ((int64_t)first_of[i] + (p - have))) : table + (b0 + i) * kv.table_ld + p;
           page[r] = ask ? *at : -1;
