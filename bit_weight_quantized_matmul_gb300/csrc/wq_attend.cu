@@ -1,4 +1,6 @@
 // wq_attend.cu -- attention over the 4-bit KV cache: which kernel, how the tokens are shared out, and the join of shared ones.
+#include <algorithm>
+
 #include "wq_attend_few.cuh"
 
 namespace wq {
@@ -99,7 +101,7 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     // Two groups of rows a block where that leaves a block for every SM, or where there is work for long (one group, two:
     // 1024 tokens of 32/8 heads of 128 over 4096 137 and 84 us, 512 of 20/20 of 64 over 8192 68 and 60; below the bound
     // 1024 of 16/16 of 128 over 1100 28 and 37, but 2 x 128 of 32/8 of 128 over 9000 88 and 63).  Tokens are shared where
-    // SMs are left, four tiles of 128 to a part at least.
+    // SMs are left, four tiles of 128 to a part at least (sinks and trees: below).
     const int64_t heads = batch * kv.heads, half = (rows + 127) / 128;
     pl.tcp.groups = heads * ((half + 1) / 2) >= kSms || half * heads * held >= (int64_t)kSms * 4096 ? 2 : 1;
     // Sinks and trees of heads of 64: one group where that is more than a block an SM, of which two fit (4 x 301 tokens behind a
@@ -108,12 +110,25 @@ Plan plan(const KvArgs& kv, int64_t batch, int64_t tokens, int64_t q_heads, int6
     if (half == 1 || (sel && kv.dim == 64 && heads * half > kSms)) pl.tcp.groups = 1;
     pl.tcp.row_tiles = (int)((half + pl.tcp.groups - 1) / pl.tcp.groups);
     // Behind a window a row tile sees what one of its tokens does and as many tokens more as it has, and a tile more for
-    // where they begin (512 tokens behind 100 of 32/8 heads of 128 21 us, two parts 27; 130 behind 400 of 32/4 24 and 21).
+    // where they begin (512 tokens behind 100 of 32/8 heads of 128 21 us, two parts 27; 130 behind 400 of 32/4 24,
+    // three parts 18).
     const int64_t wide = pl.tcp.groups * 128 / group + 1;
     const int64_t mine = sel && window > 0 && window + sinks + wide + 128 < seen ? window + sinks + wide + 128 : seen;
     const int64_t tiles = (mine + 127) / 128, most = (tiles + 3) / 4, room = kSms * ((kv.dim == 64 || sel) && pl.tcp.groups == 1 ? 2 : 1);
     int64_t want = room / (heads * pl.tcp.row_tiles);
-    if (want > most) want = most;
+    if (!sel) {
+      if (want > most) want = most;
+    } else {
+      // Sinks and trees: two tiles to a part, four past the eight parts that a warp joins, and no few parts past those (two,
+      // three, four tiles: 20 nodes over 2000 of 32/8 heads of 128 17.1, 18.4, 20.2 us, 3 x 40 over 800 .. 1500 of 8/1 of 64
+      // 15.0, 16.3, 17.9; 4 x 24 over 1000 .. 3000 of 32/8 of 128 in nine parts 31.7, in eight 25.7; 2 x 64 over 4000 .. 6000
+      // of 16/16 35 and 32).  Four tiles stay whole where the join has many rows (512 tokens behind 300 of 32/8 of 128 whole
+      // 26.7, halved 31.3, 8 x 40 over 400 .. 500 of 16/16 18.3 and 21.6; 2 x 200 behind 300 of 6/6 of 64 19.2 and 16.1).
+      want = std::min(want, (tiles + 1) / 2);
+      if (tiles <= 4 && 2 * heads * pl.tcp.row_tiles * pl.tcp.groups > kSms) want = 1;
+      if (want > kFewParts) want = std::max<int64_t>(kFewParts, std::min(want, most));
+      if (want < kFewParts + 4) want = std::min<int64_t>(want, kFewParts);
+    }
     pl.tcp.parts = (int)(want > 1 ? want : 1);
     pl.tcp.slots = pl.tcp.parts > 1 ? (size_t)(heads * pl.tcp.row_tiles * pl.tcp.parts * pl.tcp.groups * 128) : 0;
     pl.parts = pl.tcp.parts;
