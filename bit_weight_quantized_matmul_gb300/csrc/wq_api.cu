@@ -506,12 +506,27 @@ int wq_kv_keep(const wq_kv_cache* cache, const int32_t* start, int64_t batch, co
 
 int wq_tree_mask(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window, uint32_t* mask,
                  int32_t* depth, void* stream) {
-  if (batch < 0 || tokens < 0 || window < 0) return WQ_ERR_ARG;
+  return wq_tree_mask_ex(parents, batch, tokens, counts, window, 0, nullptr, mask, depth, stream);
+}
+
+int wq_tree_mask_ex(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window, int64_t sinks,
+                    const int32_t* lens, uint32_t* mask, int32_t* depth, void* stream) {
+  if (batch < 0 || tokens < 0 || window < 0 || sinks < 0) return WQ_ERR_ARG;
   if (tokens > WQ_TREE_MAX || too_many(batch, tokens)) return WQ_ERR_SHAPE;
   if (batch == 0 || tokens == 0) return WQ_OK;
-  if (!parents || !mask) return WQ_ERR_ARG;
-  if (!aligned(parents, 4) || !aligned(counts, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return WQ_ERR_ALIGN;
-  return tree_mask(parents, counts, batch, tokens, window, mask, depth, reinterpret_cast<cudaStream_t>(stream));
+  if (!parents || !mask || (window > 0 && sinks > 0 && !lens)) return WQ_ERR_ARG;
+  if (!aligned(parents, 4) || !aligned(counts, 4) || !aligned(lens, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return WQ_ERR_ALIGN;
+  TreeMaskArgs a{};
+  a.parents = parents;
+  a.counts = counts;
+  a.lens = lens;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.window = window;
+  a.sinks = sinks < (int64_t(1) << 32) ? sinks : int64_t(1) << 32;   // no more: positions are below 2^32
+  a.mask = mask;
+  a.depth = depth;
+  return tree_mask(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t wq_attend_workspace_bytes(const wq_kv_cache* cache, int64_t batch, int64_t tokens, int64_t q_heads,

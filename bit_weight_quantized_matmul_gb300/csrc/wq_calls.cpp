@@ -27,7 +27,7 @@ struct Lib {
   decltype(&wq_kv_reserve) reserve;
   decltype(&wq_kv_release) release;
   decltype(&wq_kv_keep) keep;
-  decltype(&wq_tree_mask) tree_mask;
+  decltype(&wq_tree_mask_ex) tree_mask;
 } lib;
 
 // The leading arguments of every call: (cache address, heads, dim, batch, device, stream).
@@ -297,19 +297,26 @@ PyObject* keep(const Where& w, PyObject* const* a) {
   return done(run(lib.keep, w.cache, ints(w, a[0], batch), batch, ints(w, a[1], path.numel()), path.size(1), ints(w, a[2], batch), w.stream));
 }
 
-// (parents, counts, window); no cache
-PyObject* tree_mask(const Where& w, PyObject* const* a) {
+// (parents, counts, window, sinks, lens); no cache
+PyObject* tree_mask_ex(const Where& w, PyObject* const* a) {
   const at::Tensor& parents = tensor(a[0]);
   want(parents.dim() == 2, "parents is [batch, tokens]");
-  const int64_t batch = parents.size(0), tokens = parents.size(1), window = integer(a[2]);
-  const int32_t *up = ints(w, a[0], parents.numel()), *counts = ints(w, a[1], batch);
+  const int64_t batch = parents.size(0), tokens = parents.size(1), window = integer(a[2]), sinks = integer(a[3]);
+  const int32_t *up = ints(w, a[0], parents.numel()), *counts = ints(w, a[1], batch), *lens = ints(w, a[4], batch);
   const int64_t words = (tokens + 31) / 32;
   int64_t from = 0;
   const at::Tensor whole = bytes_on(w, batch * tokens * (words + 1) * 4 + 2 * 16);
   const at::Tensor mask = part(whole, from, at::kInt, {batch, tokens, words}), depth = part(whole, from, at::kInt, {batch, tokens});
-  const int rc = run(lib.tree_mask, up, batch, tokens, counts, window, static_cast<uint32_t*>(mask.data_ptr()), static_cast<int32_t*>(depth.data_ptr()),
-                               w.stream);
+  const int rc = run(lib.tree_mask, up, batch, tokens, counts, window, sinks, lens, static_cast<uint32_t*>(mask.data_ptr()),
+                               static_cast<int32_t*>(depth.data_ptr()), w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : pair(mask, depth);
+}
+// (parents, counts, window)
+PyObject* tree_mask(const Where& w, PyObject* const* a) {
+  THPObjectPtr none(PyLong_FromLong(0));
+  if (!none.get()) throw python_error();
+  PyObject* const all[5] = {a[0], a[1], a[2], none.get(), Py_None};
+  return tree_mask_ex(w, all);
 }
 
 template <PyObject* (*F)(const Where&, PyObject* const*), int N>
@@ -361,6 +368,7 @@ PyMethodDef methods[] = {
     method<release, 5>("release"),
     method<keep, 3>("keep"),
     method<tree_mask, 3>("tree_mask"),
+    method<tree_mask_ex, 5>("tree_mask_ex"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_wq_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -202,8 +202,15 @@ struct KvKeepArgs {
 int kv_reserve(const KvReserveArgs& a, cudaStream_t s);
 int kv_release(const KvReserveArgs& a, cudaStream_t s);
 int kv_keep(const KvKeepArgs& a, cudaStream_t s);
-int tree_mask(const int32_t* parents, const int32_t* counts, int64_t batch, int64_t tokens, int64_t window, uint32_t* mask,
-              int32_t* depth, cudaStream_t s);
+struct TreeMaskArgs {
+  const int32_t* parents;      // [batch, tokens]
+  const int32_t* counts;
+  const int32_t* lens;         // read where there are a window and sinks
+  int64_t batch, tokens, window, sinks;
+  uint32_t* mask;
+  int32_t* depth;
+};
+int tree_mask(const TreeMaskArgs& a, cudaStream_t s);
 int take_status_pages();
 
 struct AttendArgs {

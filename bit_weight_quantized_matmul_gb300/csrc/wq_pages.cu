@@ -229,17 +229,17 @@ __global__ void __launch_bounds__(kMost) kv_release_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- trees
 // A thread walks up from its node.  Parents come before their children, so the ancestors' bits come out from the highest
-// word to the lowest.
-__global__ void __launch_bounds__(kMost) tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict__ counts,
-                                                          int64_t batch, int tokens, int words, int64_t window,
-                                                          uint32_t* __restrict__ mask, int32_t* __restrict__ depth) {
+// word to the lowest.  Sinks: ancestor j stays where its position, lens - counts + its depth, is below them; its depth is the
+// node's less the levels between them, so the node's is counted first, by a walk of its own.
+__global__ void __launch_bounds__(kMost) tree_mask_kernel(const __grid_constant__ TreeMaskArgs a, const int words) {
   __shared__ int16_t up[kMost];
+  const int tokens = (int)a.tokens;
   griddep_wait();
   griddep_launch_dependents();
-  for (int64_t b = blockIdx.x; b < batch; b += gridDim.x) {
-    const int n = kv::count_of(counts, b, tokens), i = threadIdx.x;
+  for (int64_t b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const int n = kv::count_of(a.counts, b, tokens), i = threadIdx.x;
     if (i < tokens) {
-      int parent = i < n ? parents[b * tokens + i] : -1;
+      int parent = i < n ? a.parents[b * tokens + i] : -1;
       if (parent < -1 || parent >= i) {
         if (i < n) set_status(WQ_STATUS_ARG);
         parent = -1;
@@ -248,18 +248,25 @@ __global__ void __launch_bounds__(kMost) tree_mask_kernel(const int32_t* __restr
     }
     __syncthreads();
     if (i < tokens) {
-      uint32_t* row = mask + (b * tokens + i) * words;
+      uint32_t* row = a.mask + (b * tokens + i) * words;
+      const bool sinks = a.window > 0 && a.sinks > 0;
+      int64_t far = 0x7FFFFFFF;                    // levels up from which on ancestors are sinks
+      if (sinks) {
+        int mine = -1;
+        for (int k = i < n ? i : -1; k >= 0; k = up[k]) ++mine;
+        far = (int64_t)max(a.lens[b], 0) - n + mine - a.sinks + 1;
+      }
       int node = i < n ? i : -1, levels = 0;
       for (int w = words - 1; w >= 0; --w) {
         uint32_t bits = 0;
         while (node >= 32 * w) {                   // never with node = -1
-          if (window == 0 || levels < window) bits |= 1u << (node & 31);
+          if (a.window == 0 || levels < a.window || (sinks && levels >= far)) bits |= 1u << (node & 31);
           ++levels;
           node = up[node];
         }
         row[w] = bits;
       }
-      if (depth) depth[b * tokens + i] = i < n ? levels - 1 : 0;
+      if (a.depth) a.depth[b * tokens + i] = i < n ? levels - 1 : 0;
     }
     __syncthreads();
   }
@@ -323,12 +330,10 @@ int launch_turn(Kernel* kernel, const KvReserveArgs& a, int64_t work, cudaStream
 int kv_reserve(const KvReserveArgs& a, cudaStream_t s) { return launch_turn(kv_reserve_kernel, a, a.tokens, s); }
 int kv_release(const KvReserveArgs& a, cudaStream_t s) { return launch_turn(kv_release_kernel, a, a.batch * a.kv.table_ld, s); }
 
-int tree_mask(const int32_t* parents, const int32_t* counts, int64_t batch, int64_t tokens, int64_t window, uint32_t* mask,
-              int32_t* depth, cudaStream_t s) {
-  const unsigned threads = (unsigned)((tokens + 31) / 32 * 32), blocks = (unsigned)(batch < 65535 ? batch : 65535);
-  if (launch_early(tree_mask_kernel, dim3(blocks), dim3(threads), 0, s, 1u, parents, counts, batch, tokens, (tokens + 31) / 32, window, mask,
-                   depth) != cudaSuccess)
-    return WQ_ERR_CUDA;
+int tree_mask(const TreeMaskArgs& a, cudaStream_t s) {
+  const int words = (int)((a.tokens + 31) / 32);
+  const unsigned blocks = (unsigned)(a.batch < 65535 ? a.batch : 65535);
+  if (launch_early(tree_mask_kernel, dim3(blocks), dim3(32 * words), 0, s, 1u, a, words) != cudaSuccess) return WQ_ERR_CUDA;
   count_launch();
   return WQ_OK;
 }

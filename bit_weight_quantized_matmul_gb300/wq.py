@@ -108,6 +108,7 @@ _SIGS = {
     "wq_kv_release": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P]),
     "wq_kv_keep": (_I, [_P, _P, _I64, _P, _I64, _P, _P]),
     "wq_tree_mask": (_I, [_P, _I64, _I64, _P, _I64, _P, _P, _P]),
+    "wq_tree_mask_ex": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P]),
     "wq_last_device_status": (_I, []),
     "wq_status_string": (ctypes.c_char_p, [_I]),
     "wq_kernel_launches": (ctypes.c_uint64, []),
@@ -313,7 +314,7 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
 
 _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
     "wq_attend", "wq_attend_ex", "wq_attend_workspace_bytes", "wq_attend_ex_workspace_bytes", "wq_kv_append", "wq_kv_append_slots",
-    "wq_kv_read", "wq_kv_reserve", "wq_kv_release", "wq_kv_keep", "wq_tree_mask")))
+    "wq_kv_read", "wq_kv_reserve", "wq_kv_release", "wq_kv_keep", "wq_tree_mask_ex")))
 
 
 def _cache_stream(cache):
@@ -400,16 +401,19 @@ def kv_keep(cache, start, path, counts=None, stream=None):
         raise WQError("wq_kv_keep", rc)
 
 
-def tree_mask(parents, counts=None, window=0, stream=None):
+def tree_mask(parents, counts=None, window=0, stream=None, sinks=0, lens=None):
     """What the nodes of drafted trees see of each other, for attend(tree=).  parents: int32 CUDA tensor [batch, tokens],
     node i's parent (before it) or -1; counts: int32 [batch] nodes of each sequence (None: all).  Returns mask int32
     [batch, tokens, ceil(tokens / 32)], whose bit j of node i is set for i itself and its ancestors (window > 0: at most
-    window - 1 levels up), and depth int32 [batch, tokens], the number of its ancestors."""
+    window - 1 levels up), and depth int32 [batch, tokens], the number of its ancestors.
+
+    sinks, lens: attend's, where there are sinks behind a window: ancestors at positions below `sinks` (lens[b] - counts[b] +
+    depth) keep their bits however many levels up they are.  Nothing checks that attend gets the same window and sinks."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return tree_mask(parents, counts, window)
+            return tree_mask(parents, counts, window, None, sinks, lens)
     index = torch._C._cuda_getDevice()
-    got = _calls.tree_mask(0, 0, 0, 0, index, _stream(), parents, counts, window)
+    got = _calls.tree_mask_ex(0, 0, 0, 0, index, _stream(), parents, counts, window, sinks, lens)
     if type(got) is int:
         raise WQError("wq_tree_mask", got)
     return got
@@ -432,8 +436,8 @@ def attend(cache, q, lens, counts=None, causal=True, window=0, scale=None, max_l
     lse fp32 [batch, tokens, q_heads].  Rows that see nothing give 0 and -inf.  workspace: a uint8 tensor of
     attend_workspace_bytes() bytes that no other call in flight uses; allocated for the call when None.
 
-    sinks: the first `sinks` tokens stay visible behind a window.  tree: (mask, depth) of tree_mask, or of one tree for all
-    sequences: q's tokens are nodes of a draft, which see the tokens before the draft (a window and sinks as from
+    sinks: the first `sinks` tokens stay visible behind a window.  tree: (mask, depth) of tree_mask (called with the same
+    window, sinks and lens), or of one tree for all sequences: q's tokens are nodes of a draft, which see the tokens before the draft (a window and sinks as from
     their depth) and of the draft what their mask says; depth None: node i is at depth i."""
     if stream is not None:                     # results and workspace are allocated on the stream that uses them
         with torch.cuda.stream(stream):

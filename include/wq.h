@@ -362,6 +362,12 @@ int wq_kv_release(const wq_kv_cache* cache, int32_t* free_pages, int64_t free_si
  * its ancestors.  Both are 0 for nodes from counts[b] on (NULL: none).  A parent that does not come before its
  * child is taken for -1, and wq_last_device_status reports WQ_ERR_ARG.  tokens <= WQ_TREE_MAX.
  *
+ * wq_tree_mask_ex: the same for attention behind a window with sinks.  An ancestor j whose position is below `sinks`,
+ * lens[b] - counts[b] + depth[j] < sinks, keeps its bit however many levels up it is: a draft behind a context shorter
+ * than the sinks sees of itself what decoding it token by token would.  lens [batch]: what each sequence holds, its
+ * draft among it, as wq_attend_ex takes it; needed with both a window and sinks (each alone changes nothing here).
+ * Nothing ties a mask to the window and the sinks that it is used with: give both calls the same.
+ *
  * wq_kv_keep: the rows of the nodes on an accepted path move up behind the context: position start[b] + path[b][i] to
  * start[b] + i for i < counts[b] (NULL: path_ld; values outside [0, path_ld] are clamped), codes and scales bit for bit,
  * all read before any is written.  path is [batch, path_ld], path_ld <= WQ_PATH_MAX.  A row whose position or place
@@ -377,6 +383,8 @@ typedef struct wq_tree {
 } wq_tree;
 int wq_tree_mask(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window,
                  uint32_t* mask, int32_t* depth, void* stream);
+int wq_tree_mask_ex(const int32_t* parents, int64_t batch, int64_t tokens, const int32_t* counts, int64_t window,
+                    int64_t sinks, const int32_t* lens, uint32_t* mask, int32_t* depth, void* stream);
 int wq_kv_keep(const wq_kv_cache* cache, const int32_t* start, int64_t batch, const int32_t* path, int64_t path_ld,
                const int32_t* counts, void* stream);
 

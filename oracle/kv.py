@@ -66,15 +66,16 @@ def attend(q, k, v, n_q, scale, causal, window=0):
     return out, lse, mean, top
 
 
-def ancestors(parents, n, window=0):
+def ancestors(parents, n, window=0, sinks=0, base=0):
     """Nodes 0 .. n-1 of a tree (parents[i] < i, or -1): bool [L, L], whether node i is or descends from j (window > 0: by
-    fewer than `window` levels), and depths [L]; nothing for nodes from n on."""
+    fewer than `window` levels, or j is among the first `sinks` tokens, the tree's roots being at position `base`), and depths
+    [L]; nothing for nodes from n on."""
     L = len(parents)
     seen, depth = np.zeros((L, L), bool), np.zeros(L, np.int32)
     for i in range(n):
         j, up = i, 0
         while j != -1:
-            seen[i, j] = window == 0 or up < window
+            seen[i, j] = window == 0 or up < window or base + depth[j] < sinks
             j, up = int(parents[j]), up + 1
         depth[i] = up - 1
     return seen, depth
