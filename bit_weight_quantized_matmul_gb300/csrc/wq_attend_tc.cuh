@@ -224,10 +224,7 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
     attend_tc_kernel(const __grid_constant__ Params p) {
   using L = Lay<D, GROUPS, SEL>;
   const AttendArgs& a = p.a;
-  if (SEL) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  if (SEL) griddep_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -296,6 +293,9 @@ __global__ void __launch_bounds__((Lay<D, GROUPS, SEL>::THREADS), (Lay<D, GROUPS
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Only now: a successor that allocates tensor memory before it waits for this kernel may take an SM's from a block that has none
+  // yet, and the two would wait for each other.
+  if (SEL) griddep_launch_dependents();
 
   const int n = kv::count_of(a.counts, b, a.tokens);
   const int len = max(a.lens[b], 0);                          // positions are counted from here

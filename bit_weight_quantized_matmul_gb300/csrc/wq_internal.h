@@ -48,7 +48,8 @@ inline bool allow_smem(std::atomic<uint64_t>& done, Kernel* kern, int bytes) {
 
 // Launches `kernel` so that it may begin while the kernel before it on the stream ends: the launch is then not waited for,
 // which is a microsecond of a call of few tokens.  The kernel calls griddep_wait() before it touches memory, and lets the next one
-// begin (griddep_launch_dependents()) only behind that: then what came before it is complete for the next one too.
+// begin (griddep_launch_dependents()) only behind that: then what came before it is complete for the next one too.  One that uses
+// tensor memory allocates it before it lets the next one begin.
 template <class... Params, class... Args>
 inline cudaError_t launch_early(void (*kernel)(Params...), dim3 blocks, dim3 threads, size_t smem, cudaStream_t s, unsigned cluster,
                                 const Args&... args) {
