@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
         const int i = x / (pieces + 1), c = x - i * (pieces + 1);
         const int node = path[i];
         if (node == i) continue;
-        const int64_t from = kv::row_of(kv, b, start + node, h, &left);
+        if (node < 0) set_status(WQ_STATUS_ARG);     // no node, though its position may well lie in the context
+        const int64_t from = node < 0 ? -1 : kv::row_of(kv, b, start + node, h, &left);
         if (from < 0) continue;
         const int64_t row = pass == 0 ? from : kv::row_of(kv, b, start + i, h, &left);
         if (row < 0) continue;

@@ -392,7 +392,8 @@ def kv_release(cache, free, top, lens, keep=None, top_out=None, stream=None):
 
 def kv_keep(cache, start, path, counts=None, stream=None):
     """The rows at start[b] + path[b, i] move to start[b] + i, i < counts[b] (None: all): an accepted path of drafted nodes
-    behind the context.  start, counts: int32 [batch]; path: int32 [batch, n], n up to WQ_PATH_MAX."""
+    behind the context.  start, counts: int32 [batch]; path: int32 [batch, n], n up to WQ_PATH_MAX.  What a negative node
+    stands for stays as it is, and last_device_status() reports it: pad short paths behind counts[b]."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_keep(cache, start, path, counts)

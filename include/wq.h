@@ -370,8 +370,8 @@ int wq_kv_release(const wq_kv_cache* cache, int32_t* free_pages, int64_t free_si
  *
  * wq_kv_keep: the rows of the nodes on an accepted path move up behind the context: position start[b] + path[b][i] to
  * start[b] + i for i < counts[b] (NULL: path_ld; values outside [0, path_ld] are clamped), codes and scales bit for bit,
- * all read before any is written.  path is [batch, path_ld], path_ld <= WQ_PATH_MAX.  A row whose position or place
- * lies outside the cache stays, and wq_last_device_status reports WQ_ERR_ARG.  Sequences must not share the pages
+ * all read before any is written.  path is [batch, path_ld], path_ld <= WQ_PATH_MAX.  A row whose node is negative, or whose
+ * position or place lies outside the cache, stays, and wq_last_device_status reports WQ_ERR_ARG.  Sequences must not share the pages
  * that are written.                                                               */
 #define WQ_TREE_MAX 1024
 #define WQ_PATH_MAX 512

@@ -306,6 +306,26 @@ def test_keep_of_rows_outside_the_cache():
     assert all(np.array_equal(raw(t), w.view(np.uint8)) for t, w in zip(case.t, want))
 
 
+@pytest.mark.parametrize("fmt", ["q4_0", "nvfp4"])
+@pytest.mark.parametrize("page", [0, 16])
+def test_keep_of_no_node(fmt, page):
+    """A node of -1 (the parent of a root, and what short paths are filled with) is no row of the context."""
+    need_gpu()
+    m, case = wq(), Case(86, fmt, 2, 64, 2, 64, page)
+    cache, before = case.upload(), [a.copy() for pair in case.rows for a in pair]
+    path = np.array([[2, 3, -1, -1, -5], [-1, 4, -2 ** 31, 6, -30]], np.int32)
+    m.kv_keep(cache, ints([30, 30]), cuda(path))
+    assert m.last_device_status() == m.WQ_ERR_ARG
+    want = [a.copy() for a in before]
+    for b, to, frm in [(0, 30, 32), (0, 31, 33), (1, 31, 34), (1, 33, 36)]:
+        (p, o), (q, r) = case.at(b, np.array([to])), case.at(b, np.array([frm]))
+        for w, a in zip(want, before):
+            w[p, :, o] = a[q, :, r]
+    assert all(np.array_equal(raw(t), w.view(np.uint8)) for t, w in zip(case.t, want))
+    m.kv_keep(cache, ints([30, 30]), cuda(path), ints([2, 0]))             # behind the counts it is not looked at
+    assert m.last_device_status() == 0
+
+
 # ------------------------------------------------------------------ a run of them
 @pytest.mark.parametrize("fmt", ["q4_0", "nvfp4"])
 def test_a_drafting_step(fmt):
