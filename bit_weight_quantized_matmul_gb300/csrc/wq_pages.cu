@@ -212,7 +212,9 @@ __global__ void __launch_bounds__(kMost) kv_release_kernel(const __grid_constant
 #pragma unroll 2
       for (int64_t e = pages + me; e < end; e += all) {
         const int i = last_at(first_of, seqs, (int)e);
-        const_cast<int32_t*>(a.free_pages)[top + e] = kv.table[(b0 + i) * kv.table_ld + have_of[i] + ((int)e - first_of[i])];
+        const int page = kv.table[(b0 + i) * kv.table_ld + have_of[i] + ((int)e - first_of[i])];
+        if ((uint32_t)page >= (uint64_t)kv.pages) set_status(WQ_STATUS_ARG);
+        const_cast<int32_t*>(a.free_pages)[top + e] = page;
       }
       __syncthreads();
     }

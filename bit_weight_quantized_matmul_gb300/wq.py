@@ -381,7 +381,8 @@ def kv_reserve(cache, free, top, lens, counts, tokens, top_out=None, out=None, s
 
 def kv_release(cache, free, top, lens, keep=None, top_out=None, stream=None):
     """The pages behind the first keep[b] tokens (None: all) of sequences that hold lens[b] go back on the stack that free and
-    top are (as in kv_reserve)."""
+    top are (as in kv_reserve).  lens[b] are the tokens that pages were granted for: last_device_status() reports numbers that are
+    none of the cache's pages.  Pages that sequences share go back once for each of them: let all but the last keep them."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_release(cache, free, top, lens, keep, top_out)

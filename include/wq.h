@@ -343,7 +343,10 @@ int wq_kv_append_slots(const wq_kv_cache* cache, const wq_heads* k, const wq_hea
  *
  * wq_kv_release: of each sequence's pages those behind its first keep[b] tokens (NULL: all of them) go back on the stack,
  * in the order of the sequences and of their pages; those past its capacity are not there.  The table is not written.
- * Pages that find no room on the stack are dropped, and wq_last_device_status reports WQ_ERR_ARG.
+ * Pages that find no room on the stack are dropped, and wq_last_device_status reports WQ_ERR_ARG.  So it does where a
+ * number that goes back is none of the cache's pages, as when lens[b] is more than was granted; it goes on the stack all
+ * the same, and whoever is given it gets slots of -1.  A page goes back once for every sequence that holds it: of several
+ * that share pages (a common prefix) all but the last one have to keep them, or the stack holds them twice.
  *
  * batch <= WQ_TURN_MAX; slots 8-byte aligned, the others 4-byte.                 */
 #define WQ_TURN_MAX 65536

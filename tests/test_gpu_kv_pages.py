@@ -151,6 +151,26 @@ def test_release(batch, ld, size):
             assert int(out) == small.numel() and small.tolist() == [-9, -9] + want[:-3] and m.last_device_status() == m.WQ_ERR_ARG
 
 
+@pytest.mark.parametrize("bad", [-1, 9, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("batch", [2, 1500])
+def test_release_of_what_is_no_page_is_reported(bad, batch):
+    """lens past what was granted: the entries behind a sequence's pages go back, and the call that takes them says so."""
+    need_gpu()
+    m, table = wq(), np.full((batch, 3), bad, np.int32)
+    table[0], table[-1] = [4, 2, bad], [7, bad, bad]
+    lens = np.zeros(batch, np.int64)
+    lens[0], lens[-1] = 32, 16
+    cache, stack, top = small_cache(16, 9, cuda(table)), torch.full((9,), -9, dtype=torch.int32, device="cuda"), ints([0])
+    m.kv_release(cache, stack, top, ints(list(lens)))
+    assert m.last_device_status() == 0 and stack[:3].tolist() == [4, 2, 7] and int(top) == 3
+    lens[-1] = 17
+    m.kv_release(cache, stack, ints([0]), ints(list(lens)), top_out=top)
+    assert m.last_device_status() == m.WQ_ERR_ARG and stack[:4].tolist() == [4, 2, 7, bad] and int(top) == 4
+    assert stack[4:].tolist() == [-9] * 5
+    m.kv_release(cache, stack, ints([0]), ints(list(lens)), ints([40] * batch), top_out=top)      # kept: not looked at
+    assert m.last_device_status() == 0 and int(top) == 0
+
+
 def test_release_then_reserve_gives_every_page_once():
     """Twenty steps of requests that come, grow and go, replayed from one graph: no page is held twice, none is lost."""
     need_gpu()
