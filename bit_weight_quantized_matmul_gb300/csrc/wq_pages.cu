@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kMost) kv_reserve_kernel(const __grid_constant
   if (what & WRITE) {
     if (me == 0) {
       if (a.starts) a.starts[a.batch] = clamp32(tokens);
-      if (a.tokens > 0 && tokens > a.tokens) set_status(WQ_STATUS_ARG);
+      if ((a.slots || a.positions) && tokens > a.tokens) set_status(WQ_STATUS_ARG);
     }
     for (int64_t k = tokens + me; k < a.tokens; k += all) {
       if (a.slots) a.slots[k] = -1;

@@ -365,7 +365,8 @@ def kv_reserve(cache, free, top, lens, counts, tokens, top_out=None, out=None, s
     """Pages for counts[b] tokens behind the lens[b] that sequence b holds, written to the cache's table, and their slots.
 
     free: int32 CUDA tensor, a stack of page numbers that nobody holds, of which the first top[0] (int32 [1]) count; lens,
-    counts: int32 [batch].  tokens: the length of the slot map, an upper bound of the sum of counts.  Returns
+    counts: int32 [batch].  tokens: the length of the slot map, an upper bound of the sum of counts (last_device_status()
+    reports one that is too small; 0 stands for no map, and reports nothing).  Returns
     (slots int64 [tokens], positions int32 [tokens], starts int32 [batch + 1], granted int32 [batch]): each token's place
     and position, all tokens laid end to end (-1 and 0 behind the last); where a sequence's begin; and counts[b], or 0
     where the pages did not last (slots -1).  out: these four, to write to.  top_out: where the number of pages left

@@ -337,8 +337,9 @@ int wq_kv_append_slots(const wq_kv_cache* cache, const wq_heads* k, const wq_hea
  *   slots      [tokens] the slot of each of these tokens, -1 without one; -1 behind the last token
  *   positions  [tokens] its position, lens[b] + i; 0 behind the last token
  *   top_out    the pages that are left; may be `top` itself
- * More tokens than `tokens` are not written, and wq_last_device_status reports WQ_ERR_ARG; so it does for a page number
- * outside the cache (slot -1).  Negative lens and counts are taken for 0.  No output may overlap an input
+ * More tokens than `tokens`, be it 0, are not written, and wq_last_device_status reports WQ_ERR_ARG (with slots and positions
+ * both NULL there is no map that could be too short, and nothing to report); so it does for a page number outside the
+ * cache (slot -1).  Negative lens and counts are taken for 0.  No output may overlap an input
  * but top_out, which may be top.
  *
  * wq_kv_release: of each sequence's pages those behind its first keep[b] tokens (NULL: all of them) go back on the stack,

@@ -124,6 +124,24 @@ def test_reserve_with_less_room_than_tokens_and_with_bad_pages():
     assert m.last_device_status() == m.WQ_ERR_ARG
 
 
+@pytest.mark.parametrize("batch", [2, 1500])
+def test_a_map_of_no_tokens_is_too_short(batch):
+    """Slots or positions are asked for, and there is no room for any: reported as any other length that does not do."""
+    need_gpu()
+    m, table = wq(), torch.full((batch, 3), -1, dtype=torch.int32, device="cuda")
+    cache, stack, top, left = small_cache(16, 9, table), ints([4, 7, 5]), ints([3]), ints([-1])
+    lens, counts, guard = ints([0] * batch), ints([5] + [0] * (batch - 1)), torch.full((4,), 77, dtype=torch.int64, device="cuda")
+    for slots, positions, status in ((guard, None, m.WQ_ERR_ARG), (None, guard, m.WQ_ERR_ARG), (None, None, 0)):
+        at = [None if x is None else x.data_ptr() for x in (slots, positions)]
+        rc = m.lib.wq_kv_reserve(cache.ref, stack.data_ptr(), 3, top.data_ptr(), left.data_ptr(), batch, lens.data_ptr(), counts.data_ptr(),
+                                 None, 0, *at, None, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and m.last_device_status() == status and int(left) == 2 and int(table[0, 0]) == 5
+    counts[0] = 0
+    rc = m.lib.wq_kv_reserve(cache.ref, stack.data_ptr(), 3, top.data_ptr(), left.data_ptr(), batch, lens.data_ptr(), counts.data_ptr(), None,
+                             0, guard.data_ptr(), None, None, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and m.last_device_status() == 0 and int(left) == 3 and guard.tolist() == [77] * 4
+
+
 @pytest.mark.parametrize("batch,ld,size", [(1, 4, 16), (40, 7, 64), (300, 90, 16), (2500, 5, 48)])
 def test_release(batch, ld, size):
     need_gpu()
