@@ -375,4 +375,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_wq_calls", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__wq_calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__wq_calls(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", WQ_CALLS_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

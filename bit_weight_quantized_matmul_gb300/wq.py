@@ -4,7 +4,8 @@ marshalling only.
 Every compute step runs in libwq's CUDA kernels.  Importing this module loads
 ``libwq.so`` from this package directory and raises ImportError when it is
 missing (build it with ``python -m bit_weight_quantized_matmul_gb300.build``);
-there is no fallback implementation.  The C entry points keep their names
+there is no fallback implementation.  Without a ``_wq_calls.so`` for this torch and
+this interpreter the KV cache calls raise ImportError.  The C entry points keep their names
 (``wq_linear`` ...); the torch helpers below allocate outputs with torch and
 pass raw device pointers plus the current CUDA stream.
 """
@@ -13,6 +14,8 @@ import os
 
 import torch
 
+from .build import calls_for
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwq.so")
 
@@ -20,11 +23,30 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libwq.so not found at {LIB_PATH}: build it first "
                       f"(python -m bit_weight_quantized_matmul_gb300.build)")
 lib = ctypes.CDLL(LIB_PATH)
-try:
-    from . import _wq_calls as _calls
-except ImportError as e:
-    raise ImportError(f"_wq_calls.so not found or not loadable in {_HERE} ({e}): build it first "
-                      f"(python -m bit_weight_quantized_matmul_gb300.build)") from e
+
+
+class _NoCalls:
+    """Stands for _wq_calls where there is none that can be used: the KV cache calls raise, all others work."""
+
+    def __init__(self, why):
+        self._why = f"_wq_calls.so in {_HERE} {why}: build it (python -m bit_weight_quantized_matmul_gb300.build)"
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
+def _load_calls():
+    try:
+        from . import _wq_calls
+    except ImportError as e:
+        return _NoCalls(f"is missing or does not load ({e})")
+    held = getattr(_wq_calls, "built_for", "something else")
+    if held != calls_for():                    # it may load all the same, with other layouts of torch's classes
+        return _NoCalls(f"was built for {held}, this is {calls_for()}")
+    return _wq_calls
+
+
+_calls = _load_calls()
 
 # ------------------------------------------------------------------ constants
 WQ_NF4, WQ_NVFP4, WQ_NVFP4_W4A4, WQ_Q4_0, WQ_Q8_0, WQ_Q4_1, WQ_Q5_0, WQ_FP8 = 1, 2, 3, 4, 5, 6, 7, 8
@@ -312,9 +334,10 @@ def kv_alloc(fmt, pages, page_size, heads, dim, table=None, k_g=None, v_g=None, 
     return KVCache(fmt, codes[0], scales[0], codes[1], scales[1], table, k_g, v_g)
 
 
-_calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-    "wq_attend", "wq_attend_ex", "wq_attend_workspace_bytes", "wq_attend_ex_workspace_bytes", "wq_kv_append", "wq_kv_append_slots",
-    "wq_kv_read", "wq_kv_reserve", "wq_kv_release", "wq_kv_keep", "wq_tree_mask_ex")))
+if not isinstance(_calls, _NoCalls):
+    _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "wq_attend", "wq_attend_ex", "wq_attend_workspace_bytes", "wq_attend_ex_workspace_bytes", "wq_kv_append", "wq_kv_append_slots",
+        "wq_kv_read", "wq_kv_reserve", "wq_kv_release", "wq_kv_keep", "wq_tree_mask_ex")))
 
 
 def _cache_stream(cache):
