@@ -11,6 +11,7 @@
 
 #include <ATen/ops/empty.h>
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/wq.h"
 
@@ -92,21 +93,38 @@ int32_t* ints(const Where& w, PyObject* o, int64_t n) { return values<int32_t>(w
 at::TensorOptions on(const Where& w, at::ScalarType type) {
   return at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(w.device));
 }
-// Outputs that are made together lie in one allocation (each of them costs as much as the launch): a contiguous tensor over the
-// part of `whole` (bytes) that begins at `from`, which moves behind it, to a multiple of 16.
-at::Tensor part(const at::Tensor& whole, int64_t& from, at::ScalarType type, at::IntArrayRef sizes) {
-  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), meta);
-  t.unsafeGetTensorImpl()->set_storage_offset(from / static_cast<int64_t>(meta.itemsize()));
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-  from += (t.numel() * static_cast<int64_t>(meta.itemsize()) + 15) / 16 * 16;
-  return t;
-}
 at::Tensor empty(at::IntArrayRef sizes, const Where& w, at::ScalarType type) {
   const Unlocked unlocked;
   return at::empty(sizes, on(w, type));
 }
-at::Tensor bytes_on(const Where& w, int64_t n) { return empty({n}, w, at::kByte); }
+// An allocation costs as much as the launch, so outputs that are made together and are small lie in one: contiguous tensors over
+// parts of it, each from a multiple of 16 bytes on.  It lives as long as one of them does, so what is larger has an allocation of
+// its own: a log-sum-exp or a few counts that are kept hold no output and no slot map alive.
+constexpr int64_t kSmall = 65536;     // bytes
+class Together {
+ public:
+  // What will be made, in this order.
+  Together(const Where& w, std::initializer_list<int64_t> bytes) : w_(w) {
+    for (const int64_t n : bytes) room_ += n <= kSmall ? rounded(n) : 0;
+  }
+  at::Tensor make(at::ScalarType type, at::IntArrayRef sizes) {
+    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+    const int64_t bytes = c10::multiply_integers(sizes) * static_cast<int64_t>(meta.itemsize());
+    if (bytes > kSmall) return empty(sizes, w_, type);
+    if (!whole_.defined()) whole_ = empty({room_}, w_, at::kByte);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole_.storage()), whole_.key_set(), meta);
+    t.unsafeGetTensorImpl()->set_storage_offset(from_ / static_cast<int64_t>(meta.itemsize()));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    from_ += rounded(bytes);
+    return t;
+  }
+
+ private:
+  static int64_t rounded(int64_t n) { return (n + 15) / 16 * 16; }
+  const Where& w_;
+  int64_t room_ = 0, from_ = 0;
+  at::Tensor whole_;
+};
 // A function of libwq.
 template <class F, class... Args>
 auto run(F* f, Args... args) {
@@ -165,10 +183,9 @@ PyObject* attend(const Where& w, PyObject* const* a) {
   const bool wants_lse = truth(a[9]);
   at::Tensor out, lse;
   if (a[7] == Py_None && wants_lse) {
-    int64_t from = 0;
-    const at::Tensor whole = bytes_on(w, q.numel() * (type == at::kFloat ? 4 : 2) + 16 + batch * tokens * q_heads * 4);
-    out = part(whole, from, type, q.sizes());
-    lse = part(whole, from, at::kFloat, {batch, tokens, q_heads});
+    Together both(w, {q.numel() * (type == at::kFloat ? 4 : 2), batch * tokens * q_heads * 4});
+    out = both.make(type, q.sizes());
+    lse = both.make(at::kFloat, {batch, tokens, q_heads});
   } else if (a[7] == Py_None) {
     out = empty(q.sizes(), w, type);
   } else {
@@ -256,10 +273,9 @@ PyObject* reserve(const Where& w, PyObject* const* a) {
   PyObject* out = a[6];
   if (out == Py_None) {
     want(tokens >= 0, "tokens is negative");
-    int64_t from = 0;
-    const at::Tensor whole = bytes_on(w, 12 * tokens + 8 * t.batch + 4 * 16);
-    const at::Tensor made[4] = {part(whole, from, at::kLong, {tokens}), part(whole, from, at::kInt, {tokens}),
-                                part(whole, from, at::kInt, {t.batch + 1}), part(whole, from, at::kInt, {t.batch})};
+    Together four(w, {8 * tokens, 4 * tokens, 4 * (t.batch + 1), 4 * t.batch});
+    const at::Tensor made[4] = {four.make(at::kLong, {tokens}), four.make(at::kInt, {tokens}), four.make(at::kInt, {t.batch + 1}),
+                                four.make(at::kInt, {t.batch})};
     out = PyTuple_New(4);
     if (!out) throw python_error();
     for (int i = 0; i < 4; ++i) {
@@ -304,9 +320,8 @@ PyObject* tree_mask_ex(const Where& w, PyObject* const* a) {
   const int64_t batch = parents.size(0), tokens = parents.size(1), window = integer(a[2]), sinks = integer(a[3]);
   const int32_t *up = ints(w, a[0], parents.numel()), *counts = ints(w, a[1], batch), *lens = ints(w, a[4], batch);
   const int64_t words = (tokens + 31) / 32;
-  int64_t from = 0;
-  const at::Tensor whole = bytes_on(w, batch * tokens * (words + 1) * 4 + 2 * 16);
-  const at::Tensor mask = part(whole, from, at::kInt, {batch, tokens, words}), depth = part(whole, from, at::kInt, {batch, tokens});
+  Together both(w, {batch * tokens * words * 4, batch * tokens * 4});
+  const at::Tensor mask = both.make(at::kInt, {batch, tokens, words}), depth = both.make(at::kInt, {batch, tokens});
   const int rc = run(lib.tree_mask, up, batch, tokens, counts, window, sinks, lens, static_cast<uint32_t*>(mask.data_ptr()),
                                static_cast<int32_t*>(depth.data_ptr()), w.stream);
   return rc != WQ_OK ? PyLong_FromLong(rc) : pair(mask, depth);

@@ -7,7 +7,9 @@ missing (build it with ``python -m bit_weight_quantized_matmul_gb300.build``);
 there is no fallback implementation.  Without a ``_wq_calls.so`` for this torch and
 this interpreter the KV cache calls raise ImportError.  The C entry points keep their names
 (``wq_linear`` ...); the torch helpers below allocate outputs with torch and
-pass raw device pointers plus the current CUDA stream.
+pass raw device pointers plus the current CUDA stream.  Outputs that a KV cache
+call makes together share one allocation if they are small (64 KB each at most):
+keeping one of them keeps the others' memory, up to that.
 """
 import ctypes
 import os
