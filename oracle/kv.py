@@ -75,7 +75,7 @@ def ancestors(parents, n, window=0, sinks=0, base=0):
     for i in range(n):
         j, up = i, 0
         while j != -1:
-            seen[i, j] = window == 0 or up < window or base + depth[j] < sinks
+            seen[i, j] = window == 0 or up < window or (sinks > 0 and base + depth[j] < sinks)
             j, up = int(parents[j]), up + 1
         depth[i] = up - 1
     return seen, depth

@@ -42,6 +42,21 @@ def test_lengths_below_the_draft():
     assert m.last_device_status() == 0
 
 
+@pytest.mark.parametrize("window,sinks", [(3, 0), (0, 4), (0, 0)])
+def test_a_window_or_sinks_alone_look_at_no_length(window, sinks):
+    need_gpu()
+    m, parents = wq(), cuda(random_trees(np.random.default_rng(7), 3, 40, 2))
+    want = m.tree_mask(parents, window=window)
+    for lens in (None, ints([40, 3, -9]), ints([45, 2 ** 31 - 1, 0])):
+        got = m.tree_mask(parents, window=window, sinks=sinks, lens=lens)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        if lens is not None and sinks == 0:
+            for b, n in enumerate(lens.tolist()):
+                seen, depth = OK.ancestors(parents[b].tolist(), 40, window, sinks, max(n, 0) - 40)
+                assert np.array_equal(got[0][b].cpu().numpy(), OK.mask_words(seen)) and np.array_equal(got[1][b].cpu().numpy(), depth)
+    assert m.last_device_status() == 0
+
+
 @FMTS
 @pytest.mark.parametrize("D,hq", [(64, 4), (128, 8)])
 @pytest.mark.parametrize("tokens", [5, 8, 40, 150])
