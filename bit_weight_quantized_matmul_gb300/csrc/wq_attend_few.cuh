@@ -60,7 +60,8 @@ constexpr int kSms = 152;
 //   q4_0   this    17.4  22.4  42.9  43.6  65.4  66.2 us     the other  44.2  43.5  43.9  43.9  44.5  45.4
 //   NVFP4  this    18.4  22.4  34.1  34.8  51.8  52.3        the other  39.2  39.3  40.3  40.6  41.1  42.3
 constexpr int kFewRows = 32;
-// Sinks and trees of q4_0 heads of 128, whose 32 rows spill here most, go there from 17 rows on (20 or 32 rows; this one, the
+// Sinks and trees of q4_0 heads of 128, whose 32 rows spill here most, go there from 17 rows on, where (c - 8) d of K is rounded to
+// 11 bits: 2^-12 of each product of a score, as wq_attend has from 33 rows on, and K is exact here (20 or 32 rows; this one, the
 // other: 8 x 8 nodes over 1000 .. 4000 38.3 and 34.4 us, 4 x 5 over 400 .. 900 22.3 and 16.5, 32 x 5 over 2000 .. 8000 182 and 185;
 // NVFP4 32 x 5 144 and 168, 64 x 8 over 1000 .. 16000 286 and 317; heads of 64, NVFP4, 16 x 24 over 1000 .. 4000 49 and 73).
 constexpr int few_rows(int fmt, int dim, bool sel) { return sel && dim == 128 && fmt == WQ_Q4_0 ? 16 : kFewRows; }

@@ -2,7 +2,7 @@
 // kernel of wq_attend_few.cuh, whose tiles are those of the first tokens and then the window's, and whose masks are words of bits.
 //
 // Measured on GB300: 64 x 1 over 1000 .. 32000 behind a window of 4096 and 4 sinks, 32/8 heads of 128 (NVFP4), 77 us with the
-// join (3.8 TB/s of 6.8 for a copy; 7 while every place is taken); 64 x 5 nodes over 1000 .. 16000 274 us; one token over 2000 behind
+// join (3.8 TB/s of 6.8 for a copy); 64 x 5 nodes over 1000 .. 16000 274 us; one token over 2000 behind
 // 256 of 20 heads of 64 7 us, bound by its dependent loads.
 #include "wq_attend_few.cuh"
 
